@@ -272,11 +272,11 @@ def exact(case, seed):
         if G > 1:
             grouped = c.reshape(T, G, E // G)
             group = grouped.topk(min(2, E // G), -1)[0].sum(-1)
-            order = group.neg().argsort(-1, stable=True)[:, :case["topk_groups"]]
+            order = group.neg().argsort(dim=-1, stable=True)[:, :case["topk_groups"]]
             allowed = torch.full((T, G, 1), -torch.inf, dtype=f, device=x.device)
             allowed.scatter_(1, order.unsqueeze(-1), 0.0)
             c = (grouped + allowed).reshape(T, E)
-        ids = c.neg().argsort(-1, stable=True)[:, :case["k"]]
+        ids = c.neg().argsort(dim=-1, stable=True)[:, :case["k"]]
         chosen = p.gather(1, ids)
         return dict(ids=None, weights=2.5 * chosen / chosen.sum(-1, keepdim=True))
     if op == "gemm":
