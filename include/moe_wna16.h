@@ -360,6 +360,120 @@ int moe_wna16_forward_noalloc(const void *x, const int32_t *topk_ids, const floa
                               moe_wna16_qparams q2, float alpha, float beta, float clamp,
                               void *out, hipStream_t stream);
 
+/*
+ * Operators around the routed layer: what makes its inputs, and the shared
+ * expert whose output is added to its own.  Same conventions as above; rows
+ * may be strided (strides count elements, innermost dimension contiguous).
+ */
+
+/* Element type of an operator's 16- or 32-bit tensors. */
+typedef enum {
+    MOE_WNA16_BF16 = 0,
+    MOE_WNA16_FP16 = 1,
+    MOE_WNA16_FP32 = 2
+} moe_wna16_dtype;
+
+/* Score function of moe_wna16_route_topk. */
+typedef enum {
+    MOE_WNA16_SOFTMAX = 0,
+    MOE_WNA16_SIGMOID = 1
+} moe_wna16_score;
+
+/*
+ * Residual addition, root-mean-square norm, and the normed rows in 8 bits
+ * with a scale for each token:
+ *   h     = x + residual, rounded to the element type (h = x without residual)
+ *   rstd  = 1 / sqrt(mean(h^2) + eps)
+ *   y     = h * weight * rstd, rounded to the element type
+ *   v     = h * weight;  m = max |v|
+ *   q     = rint(v * (127 / m)),  scale = m * rstd / 127     (y is about q * scale)
+ * rstd is common to the row, so it cancels from the codes.  FP32 arithmetic.
+ *
+ *   x            [T, H], rows x_stride apart
+ *   residual     [T, H], rows r_stride apart, or NULL
+ *   weight       [H]
+ *   residual_out [T, H] contiguous, or NULL: h.  May be x or residual itself
+ *                where that is contiguous; the tensors must not overlap otherwise
+ *   y_out        [T, H] contiguous, or NULL
+ *   q_out        [T, H] int8, rows q_stride apart, or NULL; with it
+ *   scale_out    [T] float32
+ * At least one of y_out and q_out.  Tensors aligned to their element size.
+ * T >= 0 (T = 0: no launch), 1 <= H <= 65536, strides >= H, eps >= 0 finite.
+ * A row with a NaN or infinity in v gets zero codes and a NaN scale; a row
+ * with m < 2^-100 gets zero codes and scale 0.
+ */
+int moe_wna16_add_rmsnorm(const void *x, const void *residual, const void *weight, int T, int H,
+                          int64_t x_stride, int64_t r_stride, int dtype, float eps,
+                          void *residual_out, void *y_out, int8_t *q_out, int64_t q_stride,
+                          float *scale_out, hipStream_t stream);
+
+/*
+ * Routing: router logits -> the topk_ids and topk_w that moe_wna16_forward
+ * reads.
+ *   p     = softmax(logits) over the E experts, or sigmoid(logits)
+ *   c     = p + bias (p without bias): the bias picks experts, it does not weigh
+ *   groups > 1: the experts form `groups` runs of E / groups; a group's score is
+ *         the sum of its two largest c, and only experts of the topk_groups
+ *         groups of largest score (ties to the lower group) can be picked
+ *   ids   = the topk experts of largest c, largest first, ties to the lower id
+ *   w     = p[ids] / sum(p[ids]) * scale; without renormalize p[ids] * scale
+ * p, c and the sums are carried in 64 bits.  Without bias and groups the order
+ * is that of the logits themselves.  An expert whose logit or c is -inf or NaN
+ * is never picked; slots without an expert get id -1 and weight 0 (the routed
+ * layer skips them).  A logit of +inf counts as the largest finite float.
+ * Weights are 0 where p[ids] underflows to 0.
+ *
+ *   logits  [T, E] of dtype, rows `stride` apart
+ *   bias    [E] float32, or NULL
+ *   ids_out [T, topk] int32;  w_out [T, topk] float32
+ * T >= 0 (T = 0: no launch), 1 <= E <= 1024, 1 <= topk <= min(E, 64),
+ * 1 <= groups <= 64 dividing E, 1 <= topk_groups <= groups, scale finite.
+ */
+int moe_wna16_route_topk(const void *logits, const float *bias, int T, int E, int64_t stride,
+                         int dtype, int topk, int score, int groups, int topk_groups,
+                         int renormalize, float scale, int32_t *ids_out, float *w_out,
+                         hipStream_t stream);
+
+/*
+ * Product in 8-bit integers with a scale for each token and channel:
+ *   out[t][n] = (sum_k a[t][k] w[n][k]) * a_scale[t] * w_scale[n] + addend[t][n]
+ * The sum is exact (int32); the rest is FP32, rounded once to out_dtype.
+ *
+ *   a       [T, K] int8, rows lda apart;  a_scale [T] float32
+ *   w       [N, K] int8, rows ldw apart;  w_scale [N] float32
+ *   addend  [T, N] of out_dtype, rows ld_add apart, or NULL
+ *   out     [T, N] of out_dtype, rows ldo apart; may be the addend itself
+ *           (same rows), must not overlap the inputs otherwise
+ *   workspace  moe_wna16_gemm_w8a8_workspace_size bytes, 256-byte aligned; NULL
+ *           when that is 0.  All zero before its first use; every call leaves
+ *           its counters zero.  Calls that overlap need one each.
+ * T, N >= 0 (an empty output: no launch), 1 <= K <= 131071 (the sum of 131071
+ * products of -128 * -128 is the last that fits int32), T and N up to 2^21, strides >=
+ * the row's length and below 2^23.  Operands with 16-byte aligned rows (base
+ * pointers, lda, ldw and K multiples of 16) take the fast path for T > 64.
+ */
+int moe_wna16_gemm_w8a8_workspace_size(int T, int N, int K, size_t *bytes_out);
+int moe_wna16_gemm_w8a8(const int8_t *a, const float *a_scale, const int8_t *w,
+                        const float *w_scale, const void *addend, int T, int N, int K,
+                        int64_t lda, int64_t ldw, int64_t ld_add, int64_t ldo, int out_dtype,
+                        void *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * SwiGLU (as at the top of this file) of rows [gate (I), up (I)], in 8 bits
+ * with a scale for each token:
+ *   a = g' * sigmoid(alpha * g') * (u' + beta);  m = max |a|
+ *   q = rint(a * (127 / m)),  scale = m / 127
+ *
+ *   gu     [T, 2I] of dtype, rows gu_stride apart
+ *   q_out  [T, I] int8, rows q_stride apart;  scale_out [T] float32
+ * T >= 0, 1 <= I <= 65536, strides >= the row's length; alpha, beta, clamp as
+ * in moe_wna16_forward.  Non-finite and vanishing rows as in
+ * moe_wna16_add_rmsnorm.
+ */
+int moe_wna16_swiglu_quant(const void *gu, int T, int I, int64_t gu_stride, int dtype, float alpha,
+                           float beta, float clamp, int8_t *q_out, int64_t q_stride,
+                           float *scale_out, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *moe_wna16_status_string(int status);
 

@@ -22,7 +22,9 @@ EXPORTED = ("moe_wna16_workspace_size", "moe_wna16_workspace_f32_offset",
             "moe_wna16_workspace_layout", "moe_wna16_plan",
             "moe_wna16_forward", "moe_wna16_forward_profiled", "moe_wna16_align",
             "moe_wna16_quantize", "moe_wna16_prepare", "moe_wna16_forward_prepared",
-            "moe_wna16_forward_noalloc", "moe_wna16_status_string")
+            "moe_wna16_forward_noalloc", "moe_wna16_add_rmsnorm", "moe_wna16_route_topk",
+            "moe_wna16_gemm_w8a8_workspace_size", "moe_wna16_gemm_w8a8",
+            "moe_wna16_swiglu_quant", "moe_wna16_status_string")
 
 
 class QParams(ctypes.Structure):
@@ -85,6 +87,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_wna16_forward_prepared.restype = i
     lib.moe_wna16_forward_noalloc.argtypes = lib.moe_wna16_forward.argtypes[:18] + [P]
     lib.moe_wna16_forward_noalloc.restype = i
+    i64, f = ctypes.c_int64, ctypes.c_float
+    lib.moe_wna16_add_rmsnorm.argtypes = [P, P, P, i, i, i64, i64, i, f, P, P, P, i64, P, P]
+    lib.moe_wna16_add_rmsnorm.restype = i
+    lib.moe_wna16_route_topk.argtypes = [P, P, i, i, i64, i, i, i, i, i, i, f, P, P, P]
+    lib.moe_wna16_route_topk.restype = i
+    lib.moe_wna16_gemm_w8a8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(sz)]
+    lib.moe_wna16_gemm_w8a8_workspace_size.restype = i
+    lib.moe_wna16_gemm_w8a8.argtypes = [P, P, P, P, P, i, i, i, i64, i64, i64, i64, i, P, P, sz, P]
+    lib.moe_wna16_gemm_w8a8.restype = i
+    lib.moe_wna16_swiglu_quant.argtypes = [P, i, i, i64, i, f, f, f, P, i64, P, P]
+    lib.moe_wna16_swiglu_quant.restype = i
     lib.moe_wna16_status_string.argtypes = [i]
     lib.moe_wna16_status_string.restype = ctypes.c_char_p
     _lib = lib

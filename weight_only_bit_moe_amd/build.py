@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_wna16.so")
-SOURCES = ["kernels.hip", "quantize.hip", "prepare.hip", "api.hip"]
+SOURCES = ["kernels.hip", "quantize.hip", "prepare.hip", "norm.hip", "route_topk.hip",
+           "gemm_w8a8.hip", "api.hip", "block_api.hip"]
 ARCH = "gfx950"
 
 
@@ -59,7 +60,7 @@ def build(verbose: bool = False, jobs: int = 3) -> str:
     return LIB
 
 
-# Host-side sanitizer build: the C ABI's host code (api.hip) and the oracle's C
+# Host-side sanitizer build: the C ABI's host code (api.hip, block_api.hip) and the oracle's C
 # code instrumented with AddressSanitizer and UndefinedBehaviorSanitizer, linked
 # with the other library objects into tests/sanitize/host_check (no GPU needed).
 SAN = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=all",
@@ -77,8 +78,8 @@ def build_sanitized(verbose: bool = False) -> str:
     objs = []
     for src in SOURCES:
         obj = os.path.join(bdir, src + ".o")
-        if src == "api.hip":
-            obj = os.path.join(bdir, "api.san.o")
+        if src in ("api.hip", "block_api.hip"):
+            obj = os.path.join(bdir, src.replace(".hip", ".san.o"))
             # device code as usual; every sanitizer flag applies to the host pass only
             host = [f for flag in SAN for f in ("-Xarch_host", flag)]
             _run([hipcc()] + flags() + host + ["-g", "-c", os.path.join(CSRC, src), "-o", obj],

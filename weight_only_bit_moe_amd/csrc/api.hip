@@ -8,6 +8,7 @@
 
 #include "launch.hpp"
 #include "moe_wna16.h"
+#include "ops.hpp"
 
 namespace {
 
@@ -146,6 +147,10 @@ bool offsets_fit(int T, int H, int I, int E, int topk)
 // Per-device "is gfx950" cache: 0 unknown, 1 yes, 2 no.
 std::atomic<int> g_arch_ok[64];
 
+}  // namespace
+
+namespace wna16 {
+
 int check_device()
 {
     int dev = 0;
@@ -163,6 +168,12 @@ int check_device()
     }
     return st == 1 ? MOE_WNA16_OK : MOE_WNA16_EARCH;
 }
+
+}  // namespace wna16
+
+namespace {
+
+using wna16::check_device;
 
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_WNA16_OK : MOE_WNA16_EHIP; }
 
@@ -203,7 +214,7 @@ const char *moe_wna16_status_string(int status)
     case MOE_WNA16_EINVAL: return "invalid argument (shape, null pointer or NaN parameter)";
     case MOE_WNA16_EUNSUPPORTED:
         return "unsupported configuration (bits must be 2 or 4, group 32/64/128 dividing K, "
-               "H and I multiples of 128, E <= 1024, topk <= 64)";
+               "H and I multiples of 128, E <= 1024, topk <= 64, or an operator's size limit)";
     case MOE_WNA16_EALIGN: return "misaligned pointer";
     case MOE_WNA16_EWORKSPACE: return "workspace too small";
     case MOE_WNA16_EARCH: return "current device is not gfx950 (MI355X)";

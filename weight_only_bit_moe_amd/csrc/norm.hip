@@ -1,0 +1,346 @@
+// Row kernels around the routed layer: residual addition + root-mean-square
+// norm (+ 8-bit output), and SwiGLU with 8-bit output.
+//
+// Both are one pass over memory: a workgroup owns a row, every thread keeps
+// its share of the row in registers between the reduction and the output, so
+// each input is read once and each output written once.  They are bound by
+// HBM for many rows and by the launch and one memory round trip for few.
+//
+// 8-bit rows.  With v the row before its norm's factor and m = max |v|:
+//   q = rint(v * (127 / m)),  scale = m * rstd / 127.
+// The norm's factor rstd is the same for the whole row, so it cancels from the
+// codes and enters the scale only: the codes need the maximum, not the sum of
+// squares, and both reductions share one exchange.  127 / m is rounded once
+// per row to FP32; |v * (127 / m)| <= 127 * (1 + 2^-23), so rint stays in
+// [-127, 127] and needs no clamp.  A row whose m is below 2^-100 gets zero
+// codes and scale 0 (its 127 / m would overflow further down).  The maximum is
+// taken over the magnitude bits as integers, where a NaN ranks above infinity:
+// a row with either gets zero codes and a NaN scale, which the product that
+// reads the row carries into its whole output row.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "moe_wna16.h"
+#include "ops.hpp"
+
+namespace wna16 {
+
+namespace {
+
+struct Bf16 { uint16_t u; };
+struct Fp16 { uint16_t u; };
+
+__device__ __forceinline__ float to_float(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
+__device__ __forceinline__ float to_float(Fp16 v)
+{
+    return (float)__builtin_bit_cast(_Float16, v.u);
+}
+__device__ __forceinline__ float to_float(float v) { return v; }
+
+template <class T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ Bf16 from_float<Bf16>(float v)
+{
+    return Bf16{__builtin_bit_cast(uint16_t, (__bf16)v)};   // nearest even
+}
+template <> __device__ __forceinline__ Fp16 from_float<Fp16>(float v)
+{
+    return Fp16{__builtin_bit_cast(uint16_t, (_Float16)v)};
+}
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+
+// 8 consecutive elements with the element's own alignment: rows of odd length
+// start anywhere, and gfx950 loads and stores 16 bytes at any address.
+template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Pack8 { T v[8]; };
+struct __attribute__((packed, aligned(1))) Codes8 { uint32_t lo, hi; };
+
+template <class T>
+__device__ __forceinline__ void load8(const T *p, int left, float (&f)[8])
+{
+    if (left >= 8) {
+        const Pack8<T> t = *reinterpret_cast<const Pack8<T> *>(p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = to_float(t.v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = j < left ? to_float(p[j]) : 0.f;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T *p, int left, const float (&f)[8])
+{
+    if (left >= 8) {
+        Pack8<T> t;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t.v[j] = from_float<T>(f[j]);
+        *reinterpret_cast<Pack8<T> *>(p) = t;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left)
+                p[j] = from_float<T>(f[j]);
+    }
+}
+
+__device__ __forceinline__ void store_codes(int8_t *p, int left, const float (&f)[8], float mult)
+{
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w[j >> 2] |= ((uint32_t)(int)__builtin_rintf(f[j] * mult) & 0xffu) << (8 * (j & 3));
+    if (left >= 8) {
+        *reinterpret_cast<Codes8 *>(p) = Codes8{w[0], w[1]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left)
+                p[j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
+    }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Sum and maximum over the workgroup's NT threads, the same on every thread.
+template <int NT>
+__device__ __forceinline__ void reduce(float &sum, uint32_t &top)
+{
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) {
+        sum += __shfl_xor(sum, m);
+        const uint32_t o = (uint32_t)__shfl_xor((int)top, m);
+        top = o > top ? o : top;
+    }
+    if constexpr (NT > 64) {
+        __shared__ float s[NT / 64];
+        __shared__ uint32_t t[NT / 64];
+        if ((threadIdx.x & 63) == 0) {
+            s[threadIdx.x >> 6] = sum;
+            t[threadIdx.x >> 6] = top;
+        }
+        __syncthreads();
+        sum = 0.f;
+        top = 0u;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) {
+            sum += s[i];
+            top = t[i] > top ? t[i] : top;
+        }
+    }
+}
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr uint32_t kTinyBits = 0x0d800000u;   // 2^-100
+
+// Multiplier of a row's codes from the bits of its largest magnitude.
+__device__ __forceinline__ float code_mult(uint32_t top)
+{
+    return top < kTinyBits || top >= kInfBits ? 0.f : 127.f / __uint_as_float(top);
+}
+__device__ __forceinline__ float code_scale(uint32_t top, float rstd)
+{
+    if (top >= kInfBits)
+        return __uint_as_float(0x7fc00000u);
+    return top < kTinyBits ? 0.f : __uint_as_float(top) * rstd / 127.f;
+}
+
+// NT threads own one row, R chunks of 8 elements each.
+template <class T, int NT, int R>
+__global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
+{
+    const int row = blockIdx.x;
+    const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
+    const T *w = static_cast<const T *>(a.weight);
+    const long long at = (long long)row * a.H;
+    float h[R][8];
+    float sum = 0.f;
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        load8(x + c, a.H - c, h[i]);
+    }
+    if (a.residual) {
+        const T *r = static_cast<const T *>(a.residual) + row * a.r_stride;
+        // The norm reads the sum as the residual stream stores it, so that the
+        // next step, which starts from the stored sum, sees the same rows.
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            float f[8];
+            load8(r + c, a.H - c, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                h[i][j] = to_float(from_float<T>(h[i][j] + f[j]));
+        }
+    }
+    if (a.residual_out) {
+        T *o = static_cast<T *>(a.residual_out) + at;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            store8(o + c, a.H - c, h[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        float f[8];
+        load8(w + c, a.H - c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum += h[i][j] * h[i][j];
+            h[i][j] *= f[j];                    // v from here on
+            const uint32_t m = magnitude(h[i][j]);
+            top = m > top ? m : top;
+        }
+    }
+    reduce<NT>(sum, top);
+    const float rstd = 1.f / sqrtf(sum / (float)a.H + a.eps);
+    if (a.y) {
+        T *o = static_cast<T *>(a.y) + at;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = h[i][j] * rstd;
+            store8(o + c, a.H - c, f);
+        }
+    }
+    if (a.q) {
+        const float mult = code_mult(top);
+        int8_t *o = a.q + row * a.q_stride;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            if (mult == 0.f) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    h[i][j] = 0.f;              // no inf * 0 in the codes
+            }
+            store_codes(o + c, a.H - c, h[i], mult);
+        }
+        if (threadIdx.x == 0)
+            a.scale[row] = code_scale(top, rstd);
+    }
+}
+
+// exp(-x) to about 2 ulp: x * log2(e) is split so that its rounding error,
+// which a large |x| would blow up, goes into a second exponential's linear term.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    constexpr float kLog2e = 1.44269502e+0f, kLow = 1.92596303e-8f, kLn2 = 0.693147181f;
+    const float t = -x * kLog2e;
+    const float e = __builtin_fmaf(-x, kLog2e, -t) - x * kLow;
+    const float p = __builtin_amdgcn_exp2f(t);
+    return p > 0.f && p < INFINITY ? __builtin_fmaf(p, e * kLn2, p) : p;
+}
+
+template <class T, int NT, int R>
+__global__ void __launch_bounds__(NT) swiglu_quant_kernel(SwigluArgs a)
+{
+    const int row = blockIdx.x;
+    const T *g = static_cast<const T *>(a.gu) + row * a.gu_stride;
+    const T *u = g + a.I;
+    float v[R][8], f[R][8];
+    float sum = 0.f;
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        load8(g + c, a.I - c, v[i]);
+        load8(u + c, a.I - c, f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int left = a.I - (i * NT + (int)threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // comparisons that keep a NaN (fminf would drop it)
+            const float gc = v[i][j] > a.clamp ? a.clamp : v[i][j];
+            float uc = f[i][j] > a.clamp ? a.clamp : f[i][j];
+            uc = uc < -a.clamp ? -a.clamp : uc;
+            // the hardware reciprocal (1 ulp; 1 / inf = 0)
+            const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(a.alpha * gc));
+            v[i][j] = j < left ? gc * s * (uc + a.beta) : 0.f;
+            const uint32_t m = magnitude(v[i][j]);
+            top = m > top ? m : top;
+        }
+    }
+    reduce<NT>(sum, top);
+    const float mult = code_mult(top);
+    int8_t *o = a.q + row * a.q_stride;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        if (mult == 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = 0.f;
+        }
+        store_codes(o + c, a.I - c, v[i], mult);
+    }
+    if (threadIdx.x == 0)
+        a.scale[row] = code_scale(top, 1.f);
+}
+
+// Threads and chunks per thread for rows of n elements: the fewest threads
+// that hold the row with two chunks each, up to 1024 threads, then more chunks.
+template <class F>
+hipError_t with_shape(int n, F &&f)
+{
+    const int chunks = (n + 7) / 8;
+    using std::integral_constant;
+    if (chunks <= 64)
+        f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (chunks <= 128)
+        f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (chunks <= 256)
+        f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    else if (chunks <= 512)
+        f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (chunks <= 1024)
+        f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (chunks <= 2048)
+        f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else if (chunks <= 4096)
+        f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+    else
+        f(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const NormArgs &a, int dtype, hipStream_t stream)
+{
+    return with_shape(a.H, [&](auto nt, auto r) {
+        constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+        if (dtype == MOE_WNA16_BF16)
+            add_rmsnorm_kernel<Bf16, NT, R><<<a.T, NT, 0, stream>>>(a);
+        else if (dtype == MOE_WNA16_FP16)
+            add_rmsnorm_kernel<Fp16, NT, R><<<a.T, NT, 0, stream>>>(a);
+        else
+            add_rmsnorm_kernel<float, NT, R><<<a.T, NT, 0, stream>>>(a);
+    });
+}
+
+hipError_t launch_swiglu_quant(const SwigluArgs &a, int dtype, hipStream_t stream)
+{
+    return with_shape(a.I, [&](auto nt, auto r) {
+        constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+        if (dtype == MOE_WNA16_BF16)
+            swiglu_quant_kernel<Bf16, NT, R><<<a.T, NT, 0, stream>>>(a);
+        else if (dtype == MOE_WNA16_FP16)
+            swiglu_quant_kernel<Fp16, NT, R><<<a.T, NT, 0, stream>>>(a);
+        else
+            swiglu_quant_kernel<float, NT, R><<<a.T, NT, 0, stream>>>(a);
+    });
+}
+
+}  // namespace wna16
