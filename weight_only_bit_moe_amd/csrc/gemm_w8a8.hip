@@ -192,21 +192,32 @@ __device__ __forceinline__ void copy16_to_lds(const int8_t *base_in, uint32_t vo
 }
 #pragma clang diagnostic pop
 
-// Tile of BM tokens x BN channels, WM x WN waves, K in chunks of 128 bytes.
-// Operand rows of 128 bytes sit in LDS as 8 pieces of 16 bytes; piece c of row
-// r is stored at place c ^ ((r >> 1) & 7), so that the 16 rows that one MFMA
-// operand read touches are spread over all banks.  Two stages: the copies of
-// chunk i + 1 run while chunk i is multiplied.
+// Tile of BM tokens x BN channels, WM x WN waves, K in chunks of 128 bytes
+// (two MFMA steps).  Operand rows of 128 bytes sit in LDS as 8 pieces of 16
+// bytes; piece c of row r is stored at place c ^ ((r >> 1) & 7), so that the
+// 16 rows that one operand read touches cover all banks once.
+//
+// Pipeline, two LDS stages and two sets of operand registers.  While the
+// first step of chunk c is multiplied, the second step's operands are read;
+// then one barrier: every wave holds all it needs of chunk c, and chunk c + 1
+// has arrived; while the second step is multiplied, chunk c + 2 is copied over
+// chunk c and the first operands of chunk c + 1 are read.
 template <int BM_, int BN_, int WM_, int WN_>
 struct Tile8 {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
     static constexpr int KC = 128;
     static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     static constexpr int STAGE = (BM + BN) * KC;
-    static constexpr int COPIES = (BM + BN) / 8 / NW;     // 8 rows per copy
+    static constexpr int ACOPIES = BM / 8 / NW, COPIES = (BM + BN) / 8 / NW;   // 8 rows each
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0, "copies divide evenly");
+    // epilogue: each wave stages rows of its BN / WN channels
+    static constexpr int WCOLS = BN / WN, REGION = 2 * STAGE / NW;
 
     static __device__ __forceinline__ int place(int row, int c) { return c ^ ((row >> 1) & 7); }
+
+    struct Frag {
+        v4i a[MT], b[NT];
+    };
 
     template <class T>
     static __device__ __forceinline__ void run(const GemmArgs &g, int t0, int n0, char *lds)
@@ -214,33 +225,35 @@ struct Tile8 {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
-        const uint32_t lds0 = lds_of(lds);
-        // Copies: copy i of this wave brings rows [8 * (i * NW + wave), +8).
-        // Rows past the end repeat the last row; their results are dropped.
+        const uint32_t lds0 = lds_of(lds) + wave * 1024;
+        // Copy i of this wave brings rows [8 * (i * NW + wave), +8).  Rows past
+        // the end repeat the last row; their results are dropped.
         uint32_t off[COPIES];
-        const int8_t *base[2] = {g.a + (long long)t0 * g.lda, g.w + (long long)n0 * g.ldw};
         const int crow = lane >> 3;
+        const int cplace = place(wave * 8 + crow, lane & 7) * 16;   // the same for every copy
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            const int row = (i * NW + wave) * 8 + crow;
-            const bool is_a = i < BM / 8 / NW;
-            const int rr = is_a ? row : row - BM;
+            const bool is_a = i < ACOPIES;
+            const int row = ((is_a ? i : i - ACOPIES) * NW + wave) * 8 + crow;
             const int last = is_a ? g.T - 1 - t0 : g.N - 1 - n0;
-            off[i] = (uint32_t)((rr < last ? rr : last) * (is_a ? g.lda : g.ldw)) +
-                     (uint32_t)place(row, lane & 7) * 16;
+            off[i] = (uint32_t)((row < last ? row : last) * (is_a ? g.lda : g.ldw)) +
+                     (uint32_t)cplace;
         }
-        // K past the end (a multiple of 16): the piece's first one is read
-        // again and the channel operand's fragment is cleared below.
-        auto copy = [&](int k, int stage) {
+        const int8_t *abase = g.a + (long long)t0 * g.lda, *wbase = g.w + (long long)n0 * g.ldw;
+        const int r = lane & 15, kq = lane >> 4;
+        const int arow = wm * (MT * 16) + r, brow = BM + wn * (NT * 16) + r;
+        // place() of the lane's rows is the same for every 16-row step
+        const char *at[2] = {lds + arow * KC + place(arow, kq) * 16,
+                             lds + arow * KC + place(arow, 4 + kq) * 16};
+        const char *bt[2] = {lds + brow * KC + place(brow, kq) * 16,
+                             lds + brow * KC + place(brow, 4 + kq) * 16};
+        auto read = [&](Frag &f, int stage, int s) {
 #pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-                const int row = (i * NW + wave) * 8 + crow;
-                const int kk = k + place(row, lane & 7) * 16;
-                const uint32_t o = kk < g.K ? off[i] + (uint32_t)k
-                                            : off[i] - (uint32_t)place(row, lane & 7) * 16;
-                copy16_to_lds(base[i < BM / 8 / NW ? 0 : 1], o,
-                              lds0 + stage * STAGE + (i * NW + wave) * 1024);
-            }
+            for (int n = 0; n < NT; ++n)
+                f.b[n] = *reinterpret_cast<const v4i *>(bt[s] + stage * STAGE + n * 16 * KC);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                f.a[m] = *reinterpret_cast<const v4i *>(at[s] + stage * STAGE + m * 16 * KC);
         };
         v4i acc[NT][MT];
 #pragma unroll
@@ -248,64 +261,208 @@ struct Tile8 {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 acc[n][m] = v4i{0, 0, 0, 0};
-        const int r = lane & 15, kq = lane >> 4;
-        const int arow = wm * (MT * 16) + r, brow = BM + wn * (NT * 16) + r;
-        copy(0, 0);
+        auto multiply = [&](const Frag &f) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n][m] =
+                        __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[n], f.a[m], acc[n][m], 0, 0, 0);
+        };
+        auto clear_past_k = [&](Frag &f, int k) {
+            if (k + kq * 16 >= g.K) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    f.b[n] = v4i{0, 0, 0, 0};
+            }
+        };
         const int chunks = (g.K + KC - 1) / KC;
-        for (int c = 0; c < chunks; ++c) {
-            __builtin_amdgcn_s_waitcnt(0x0f70);        // vmcnt(0): this chunk has arrived
+        // The loop's copies are whole chunks; the last chunk may be a part.
+        auto copy_whole = [&](int c) {
+            const uint32_t st = lds0 + (c & 1) * STAGE;
+            const int8_t *a = abase + (long long)c * KC, *w = wbase + (long long)c * KC;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i)
+                copy16_to_lds(i < ACOPIES ? a : w, off[i], st + i * NW * 1024);
+        };
+        auto copy_any = [&](int c) {
+            if ((c + 1) * KC <= g.K) {
+                copy_whole(c);
+                return;
+            }
+            // K past the end (K is a multiple of 16): the row's first piece is
+            // read again, and the channel operand's registers are cleared below
+            const uint32_t st = lds0 + (c & 1) * STAGE;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+                const bool in = c * KC + cplace < g.K;
+                copy16_to_lds(i < ACOPIES ? abase : wbase,
+                              in ? off[i] + (uint32_t)(c * KC) : off[i] - (uint32_t)cplace,
+                              st + i * NW * 1024);
+            }
+        };
+        Frag f0, f1;
+        copy_any(0);
+        __builtin_amdgcn_s_waitcnt(0x0f70);                // vmcnt(0)
+        __syncthreads();
+        if (chunks > 1)
+            copy_any(1);
+        read(f0, 0, 0);
+        int c = 0;
+        for (; c + 2 < chunks; ++c) {
+            read(f1, c & 1, 1);
+            multiply(f0);
+            __builtin_amdgcn_s_waitcnt(0x0f70);            // chunk c + 1 has arrived
+            __syncthreads();
+            copy_any(c + 2);
+            read(f0, (c + 1) & 1, 0);
+            multiply(f1);
+        }
+        for (; c < chunks; ++c) {                          // the last two
+            read(f1, c & 1, 1);
+            clear_past_k(f0, c * KC);
+            multiply(f0);
+            __builtin_amdgcn_s_waitcnt(0x0f70);
             __syncthreads();
             if (c + 1 < chunks)
-                copy((c + 1) * KC, (c + 1) & 1);
-            const char *st = lds + (c & 1) * STAGE;
-            const bool tail = (c + 1) * KC > g.K;
+                read(f0, (c + 1) & 1, 0);
+            clear_past_k(f1, c * KC + 64);
+            multiply(f1);
+        }
+        epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, lds + wave * REGION);
+    }
+
+    // A lane holds four consecutive channels of one token per 16 x 16 result:
+    // written straight to memory, an instruction would touch 16 rows with 32
+    // bytes each.  The wave's rows go through its own part of LDS instead (free:
+    // the loop's last barrier is past every read), and leave as whole runs of
+    // WCOLS elements, 16 bytes a lane.  Pieces of 16 bytes are swizzled as the
+    // operands are.
+    template <class T>
+    static __device__ __forceinline__ void epilogue(const GemmArgs &g, int t0, int n0,
+                                                    const v4i (&acc)[NT][MT], char *region)
+    {
+        constexpr int ROW = WCOLS * sizeof(T), PIECES = ROW / 16, EPP = 16 / sizeof(T);
+        constexpr int MP = MT < 2 ? MT : 2;   // 16-row steps a pass
+        static_assert(MT % MP == 0 && PIECES >= 8 && MP * 16 * ROW <= REGION, "passes fit");
+        const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
+        float sw[NT][4];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                v4i fa[MT], fb[NT];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    fa[m] = *reinterpret_cast<const v4i *>(
-                        st + (arow + m * 16) * KC + place(arow + m * 16, s * 4 + kq) * 16);
+            for (int i = 0; i < 4; ++i) {
+                const int col = n0 + n * 16 + kq * 4 + i;
+                sw[n][i] = g.w_scale[col < g.N ? col : g.N - 1];
+            }
+        float sa[MT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    fb[n] = *reinterpret_cast<const v4i *>(
-                        st + (brow + n * 16) * KC + place(brow + n * 16, s * 4 + kq) * 16);
-                if (tail && c * KC + s * 64 + kq * 16 >= g.K) {
+        for (int m = 0; m < MT; ++m)
+            sa[m] = g.a_scale[t0 + m * 16 + r < g.T ? t0 + m * 16 + r : g.T - 1];
+#pragma unroll
+        for (int p = 0; p < MT / MP; ++p) {
+            Out4<T> add[MP][NT];
+            if (g.addend) {
+#pragma unroll
+                for (int mm = 0; mm < MP; ++mm)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        fb[n] = v4i{0, 0, 0, 0};
+                        add[mm][n] = load_addend<T>(g, t0 + (p * MP + mm) * 16 + r,
+                                                    n0 + n * 16 + kq * 4);
+            }
+#pragma unroll
+            for (int mm = 0; mm < MP; ++mm) {
+                const int m = p * MP + mm, row = mm * 16 + r;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int byte = (n * 16 + kq * 4) * (int)sizeof(T);
+                    char *at = region + row * ROW + (((byte >> 4) ^ ((row >> 1) & 7)) << 4) +
+                               (byte & 15);
+                    Out4<T> v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float f = (float)acc[n][m][i] * sa[m] * sw[n][i];
+                        if (g.addend)
+                            f += widen(add[mm][n].v[i]);
+                        v.v[i] = narrow<T>(f);
+                    }
+                    if constexpr (sizeof(T) == 4)
+                        *reinterpret_cast<v4i *>(at) = __builtin_bit_cast(v4i, v);
+                    else
+                        *reinterpret_cast<uint64_t *>(at) = __builtin_bit_cast(uint64_t, v);
                 }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            constexpr int STEPS = MP * 16 * PIECES / 64;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < STEPS; ++i) {
+                const int id = i * 64 + lane, row = id / PIECES, c = id % PIECES;
+                const int t = t0 + p * MP * 16 + row, n = n0 + c * EPP;
+                const v4i v = *reinterpret_cast<const v4i *>(region + row * ROW +
+                                                             ((c ^ ((row >> 1) & 7)) << 4));
+                store_piece<T>(g, t, n, v);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+
+    template <class T>
+    static __device__ __forceinline__ Out4<T> load_addend(const GemmArgs &g, int t, int n)
+    {
+        Out4<T> r{};
+        if (t < g.T && n < g.N) {
+            const T *p = static_cast<const T *>(g.addend) + t * g.ld_add + n;
+            if (n + 4 <= g.N) {
+                r = *reinterpret_cast<const Out4<T> *>(p);
+            } else {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        acc[n][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[n], fa[m], acc[n][m],
-                                                                          0, 0, 0);
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < g.N)
+                        r.v[i] = p[i];
             }
         }
+        return r;
+    }
+
+    template <class T>
+    static __device__ __forceinline__ void store_piece(const GemmArgs &g, int t, int n, v4i v)
+    {
+        constexpr int EPP = 16 / sizeof(T);
+        if (t >= g.T || n >= g.N)
+            return;
+        struct __attribute__((packed, aligned(sizeof(T)))) Piece { T v[EPP]; };
+        Piece x = __builtin_bit_cast(Piece, v);
+        T *o = static_cast<T *>(g.out) + t * g.ldo + n;
+        if (n + EPP <= g.N) {
+            *reinterpret_cast<Piece *>(o) = x;
+        } else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = t0 + arow + m * 16;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int v[4] = {acc[n][m][0], acc[n][m][1], acc[n][m][2], acc[n][m][3]};
-                emit4<T>(g, t, n0 + wn * (NT * 16) + n * 16 + kq * 4, v);
-            }
+            for (int i = 0; i < EPP; ++i)
+                if (n + i < g.N)
+                    o[i] = x.v[i];
         }
     }
 };
 
+constexpr int kBand = 8;
+
 template <class C, class T>
-__global__ void __launch_bounds__(64 * C::NW) gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
+__global__ void __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
+gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
 {
     __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
     // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of
-    // tiles, so its L2 serves neighbours that share an operand.
+    // tiles, so its L2 serves neighbours that share an operand: tiles are
+    // numbered down bands of kBand rows, so that the 32 an XCD runs at a time
+    // are about as many rows as columns.
     const int total = tiles_m * tiles_n, per = (total + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (id >= total || (int)(blockIdx.x >> 3) >= per)
         return;
-    const int tm = id / tiles_n, tn = id % tiles_n;
+    const int band = id / (kBand * tiles_n), rest = id - band * (kBand * tiles_n);
+    const int rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
+    const int tm = band * kBand + rest % rows, tn = rest / rows;
     C::template run<T>(g, tm * C::BM, tn * C::BN, lds);
 }
 
