@@ -8,28 +8,13 @@
 
 #include "moe_wna16.h"
 #include "ops.hpp"
+#include "wave.hpp"
 
 namespace wna16 {
 
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-
-struct GBf16 { uint16_t u; };
-struct GFp16 { uint16_t u; };
-__device__ __forceinline__ float widen(GBf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
-__device__ __forceinline__ float widen(GFp16 v) { return (float)__builtin_bit_cast(_Float16, v.u); }
-__device__ __forceinline__ float widen(float v) { return v; }
-template <class T> __device__ __forceinline__ T narrow(float v);
-template <> __device__ __forceinline__ GBf16 narrow<GBf16>(float v)
-{
-    return GBf16{__builtin_bit_cast(uint16_t, (__bf16)v)};
-}
-template <> __device__ __forceinline__ GFp16 narrow<GFp16>(float v)
-{
-    return GFp16{__builtin_bit_cast(uint16_t, (_Float16)v)};
-}
-template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 
 template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Out4 { T v[4]; };
 
@@ -51,18 +36,18 @@ __device__ __forceinline__ void emit4(const GemmArgs &g, int t, int n, const int
             const Out4<T> d = *reinterpret_cast<const Out4<T> *>(add);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                f[i] += widen(d.v[i]);
+                f[i] += to_float(d.v[i]);
         }
         Out4<T> r;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r.v[i] = narrow<T>(f[i]);
+            r.v[i] = from_float<T>(f[i]);
         *reinterpret_cast<Out4<T> *>(o) = r;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (n + i < g.N)
-                o[i] = narrow<T>(add ? f[i] + widen(add[i]) : f[i]);
+                o[i] = from_float<T>(add ? f[i] + to_float(add[i]) : f[i]);
     }
 }
 
@@ -156,9 +141,9 @@ __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_
         const int v[4] = {sum[0], sum[1], sum[2], sum[3]};
         const int t = t0 + m * 16 + r, n = n0 + (lane >> 4) * 4;
         if (out_dtype == MOE_WNA16_BF16)
-            emit4<GBf16>(g, t, n, v);
+            emit4<Bf16>(g, t, n, v);
         else if (out_dtype == MOE_WNA16_FP16)
-            emit4<GFp16>(g, t, n, v);
+            emit4<Fp16>(g, t, n, v);
         else
             emit4<float>(g, t, n, v);
     }
@@ -382,8 +367,8 @@ struct Tile8 {
                     for (int i = 0; i < 4; ++i) {
                         float f = (float)acc[n][m][i] * sa[m] * sw[n][i];
                         if (g.addend)
-                            f += widen(add[mm][n].v[i]);
-                        v.v[i] = narrow<T>(f);
+                            f += to_float(add[mm][n].v[i]);
+                        v.v[i] = from_float<T>(f);
                     }
                     if constexpr (sizeof(T) == 4)
                         *reinterpret_cast<v4i *>(at) = __builtin_bit_cast(v4i, v);
@@ -476,9 +461,9 @@ hipError_t launch_tile(const GemmArgs &g, int out_dtype, hipStream_t stream)
         return hipGetLastError();
     };
     if (out_dtype == MOE_WNA16_BF16)
-        return go(gemm_tile_kernel<C, GBf16>);
+        return go(gemm_tile_kernel<C, Bf16>);
     if (out_dtype == MOE_WNA16_FP16)
-        return go(gemm_tile_kernel<C, GFp16>);
+        return go(gemm_tile_kernel<C, Fp16>);
     return go(gemm_tile_kernel<C, float>);
 }
 

@@ -23,31 +23,11 @@
 
 #include "moe_wna16.h"
 #include "ops.hpp"
+#include "wave.hpp"
 
 namespace wna16 {
 
 namespace {
-
-struct Bf16 { uint16_t u; };
-struct Fp16 { uint16_t u; };
-
-__device__ __forceinline__ float to_float(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
-__device__ __forceinline__ float to_float(Fp16 v)
-{
-    return (float)__builtin_bit_cast(_Float16, v.u);
-}
-__device__ __forceinline__ float to_float(float v) { return v; }
-
-template <class T> __device__ __forceinline__ T from_float(float v);
-template <> __device__ __forceinline__ Bf16 from_float<Bf16>(float v)
-{
-    return Bf16{__builtin_bit_cast(uint16_t, (__bf16)v)};   // nearest even
-}
-template <> __device__ __forceinline__ Fp16 from_float<Fp16>(float v)
-{
-    return Fp16{__builtin_bit_cast(uint16_t, (_Float16)v)};
-}
-template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
 
 // 8 consecutive elements with the element's own alignment: rows of odd length
 // start anywhere, and gfx950 loads and stores 16 bytes at any address.
@@ -108,12 +88,8 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 template <int NT>
 __device__ __forceinline__ void reduce(float &sum, uint32_t &top)
 {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) {
-        sum += __shfl_xor(sum, m);
-        const uint32_t o = (uint32_t)__shfl_xor((int)top, m);
-        top = o > top ? o : top;
-    }
+    sum = wave_sum(sum);
+    top = wave_max(top);
     if constexpr (NT > 64) {
         __shared__ float s[NT / 64];
         __shared__ uint32_t t[NT / 64];
@@ -127,7 +103,7 @@ __device__ __forceinline__ void reduce(float &sum, uint32_t &top)
 #pragma unroll
         for (int i = 0; i < NT / 64; ++i) {
             sum += s[i];
-            top = t[i] > top ? t[i] : top;
+            top = larger(top, t[i]);
         }
     }
 }
@@ -163,6 +139,17 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
         const int c = (i * NT + (int)threadIdx.x) * 8;
         load8(x + c, a.H - c, h[i]);
     }
+    // Every load before the first store: a store could alias the weight, and the
+    // load behind it would be another round trip.  (Longer rows reload it.)
+    constexpr bool kHold = R <= 2;
+    float wt[kHold ? R : 1][8];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * NT + (int)threadIdx.x) * 8;
+            load8(w + c, a.H - c, wt[i]);
+        }
+    }
     if (a.residual) {
         const T *r = static_cast<const T *>(a.residual) + row * a.r_stride;
         // The norm reads the sum as the residual stream stores it, so that the
@@ -188,14 +175,13 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int c = (i * NT + (int)threadIdx.x) * 8;
-        float f[8];
-        load8(w + c, a.H - c, f);
+        if constexpr (!kHold)
+            load8(w + c, a.H - c, wt[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             sum += h[i][j] * h[i][j];
-            h[i][j] *= f[j];                    // v from here on
-            const uint32_t m = magnitude(h[i][j]);
-            top = m > top ? m : top;
+            h[i][j] *= wt[kHold ? i : 0][j];    // v from here on
+            top = larger(top, magnitude(h[i][j]));
         }
     }
     reduce<NT>(sum, top);
@@ -268,8 +254,7 @@ __global__ void __launch_bounds__(NT) swiglu_quant_kernel(SwigluArgs a)
             // the hardware reciprocal (1 ulp; 1 / inf = 0)
             const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(a.alpha * gc));
             v[i][j] = j < left ? gc * s * (uc + a.beta) : 0.f;
-            const uint32_t m = magnitude(v[i][j]);
-            top = m > top ? m : top;
+            top = larger(top, magnitude(v[i][j]));
         }
     }
     reduce<NT>(sum, top);

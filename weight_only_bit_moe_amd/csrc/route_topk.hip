@@ -12,14 +12,20 @@
 // id -1 and weight 0, which the routed layer skips.  A logit of +inf counts as
 // the largest finite one.
 //
-// Which of two nearly equal c is ahead decides which expert runs, so p, c and
-// the groups' sums are carried in 64 bits: two experts swap only if they agree
-// to about 2^-52.  Without bias and groups the order of c is the order of the
-// logits, so no p is computed before the experts are picked.
+// Which of two nearly equal c is ahead decides which expert runs, so the order
+// is that of 64-bit scores: two experts swap only if they agree to about 2^-52.
+// Most tokens need no 64-bit score for it.  The scores are first taken in
+// 32 bits, where they are off by less than 2^-19 (1 + |c|), and the token keeps
+// that order if every comparison that mattered was wider than the two errors:
+// consecutive picks, the last pick and the first expert left out, and any two
+// groups.  Otherwise the wave repeats the picking in 64 bits.  Without bias and
+// groups the order of c is the order of the logits, which is exact in 32 bits.
+// The weights of the picked experts are always computed in 64 bits.
 //
 // One wave owns a token; lane i holds experts [i*EPL, (i+1)*EPL).  Picking is
-// topk rounds of a wave-wide maximum over order-preserving 64-bit keys, each
-// round taking the lowest lane and slot that hold the maximum.
+// rounds of a wave-wide maximum (DPP, no LDS), each taking the lowest lane and
+// slot that hold the maximum.  With one token the time is the chain of memory
+// round trips and reductions; with many it is the VALU instructions per token.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -27,6 +33,7 @@
 
 #include "moe_wna16.h"
 #include "ops.hpp"
+#include "wave.hpp"
 
 namespace wna16 {
 
@@ -34,172 +41,255 @@ namespace {
 
 constexpr int kWaves = 4;   // tokens per workgroup
 
-struct RBf16 { uint16_t u; };
-struct RFp16 { uint16_t u; };
-__device__ __forceinline__ float logit(RBf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
-__device__ __forceinline__ float logit(RFp16 v) { return (float)__builtin_bit_cast(_Float16, v.u); }
-__device__ __forceinline__ float logit(float v) { return v; }
-
-// Order-preserving map of the doubles above -inf to integers above 0; out
-// (0) for -inf and NaN.  -0 and +0 get the same key.
-__device__ __forceinline__ uint64_t key_of(double c)
-{
-    if (!(c > -(double)INFINITY))
-        return 0;
-    const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);
-    return b >> 63 ? ~b : b | (1ull << 63);
-}
-
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m)
-{
-    return __builtin_bit_cast(uint64_t, __shfl_xor(__builtin_bit_cast(double, v), m));
-}
-
-__device__ __forceinline__ uint64_t wave_max(uint64_t v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = shfl_xor64(v, m);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-
-__device__ __forceinline__ double wave_sum(double v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        v += __shfl_xor(v, m);
-    return v;
-}
-
+// exp(l - top) or sigmoid(l)
 template <bool SOFTMAX>
-__device__ __forceinline__ double score_of(float l, float top)
+__device__ __forceinline__ double score_of(float l, float top, double)
 {
     if constexpr (SOFTMAX)
         return exp((double)l - (double)top);
     else
         return 1.0 / (1.0 + exp(-(double)l));
 }
+template <bool SOFTMAX>
+__device__ __forceinline__ float score_of(float l, float top, float)
+{
+    constexpr float kLog2e = 1.44269504f;
+    if constexpr (SOFTMAX)
+        return __builtin_amdgcn_exp2f((l - top) * kLog2e);
+    else
+        return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * -kLog2e));
+}
+
+// Whether two 32-bit scores may be in another order in 64 bits.  A sigmoid is
+// off by less than 4 FP32 roundings; a softmax by up to 8 of its own and 22 of
+// the sum (16 scores a lane, then 6 steps); adding the bias is one more.  So a
+// score is off by less than 2^-19 (1 + |c|), a group's sum of two by twice that.
+__device__ __forceinline__ bool too_near(float a, float b, float tolerance)
+{
+    return __builtin_fabsf(a - b) <= tolerance * (1.f + __builtin_fabsf(b));
+}
+__device__ __forceinline__ bool too_near(double, double, float) { return false; }
+
+template <class C, int EPL>
+__device__ __forceinline__ C top_of(const C (&c)[EPL])
+{
+    C v = c[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j)
+        v = larger(v, c[j]);
+    return v;
+}
+
+// Takes the experts outside the best groups out of c.  Returns whether two
+// groups were too near to tell apart.
+template <class C, int EPL>
+__device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int lane, C *row)
+{
+    const C kOut = -(C)INFINITY;
+    const int per = a.E / a.groups, span = per / EPL;
+    bool near = false;
+    // a group's two largest; with one expert left (or one in all) that one
+    auto total = [&](C one, C two) { return two > kOut ? one + two : one; };
+    auto count = [&](C score, int mine, auto &&of) {
+        int ahead = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const C o = of(g);
+            ahead += o > score || (o == score && g < mine) ? 1 : 0;
+            near |= g != mine && o > kOut && score > kOut && too_near(o, score, 0x1p-17f);
+        }
+        return ahead;
+    };
+    if (span * EPL == per && (span == 2 || span == 4 || span == 8 || span == 16)) {
+        // groups are whole runs of lanes: merge the lanes' pairs by permutes
+        C one = kOut, two = kOut;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            two = c[j] > one ? one : larger(two, c[j]);
+            one = larger(one, c[j]);
+        }
+        auto merge = [&](C o1, C o2) {
+            two = o1 > one ? larger(one, o2) : larger(two, o1);
+            one = larger(one, o1);
+        };
+        merge(dpp<kXor1>(one), dpp<kXor1>(two));
+        if (span >= 4)
+            merge(dpp<kXor2>(one), dpp<kXor2>(two));
+        if (span >= 8)
+            merge(dpp<kHalfMirror>(one), dpp<kHalfMirror>(two));
+        if (span >= 16)
+            merge(dpp<kMirror>(one), dpp<kMirror>(two));
+        const C score = total(one, two);
+        const int mine = lane / span;
+        const int ahead = count(score, mine, [&](int g) { return lane_value(score, g * span); });
+        if (ahead >= a.topk_groups) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                c[j] = kOut;
+        }
+        near = near && mine < a.groups;
+    } else {
+        // any other shape: lane g reads group g's scores
+        const int e0 = lane * EPL;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            row[e0 + j] = c[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        C one = kOut, two = kOut;
+        if (lane < a.groups)
+            for (int i = 0; i < per; ++i) {
+                const C v = row[lane * per + i];
+                two = v > one ? one : larger(two, v);
+                one = larger(one, v);
+            }
+        const C score = total(one, two);
+        const int ahead = count(score, lane, [&](int g) { return lane_value(score, g); });
+        const uint64_t keep = __ballot(lane < a.groups && ahead < a.topk_groups);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (e0 + j < a.E && !((keep >> ((e0 + j) / per)) & 1))
+                c[j] = kOut;
+        near = near && lane < a.groups;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    return __ballot(near) != 0;
+}
+
+// Picks the topk largest of c: lane r gets the r-th pick and its logit.
+// Returns whether two that had to be told apart were too near.
+template <class C, int EPL>
+__device__ __forceinline__ bool pick(C (&c)[EPL], const float (&l)[EPL], int topk, bool check,
+                                     int lane, int &mine, float &logit_of_mine)
+{
+    const C kOut = -(C)INFINITY;
+    mine = -1;
+    bool near = false;
+    C last = (C)INFINITY;
+    const int rounds = check ? topk + 1 : topk;     // one more: the first left out
+    for (int r = 0; r < rounds; ++r) {
+        const C best = top_of<C, EPL>(c);
+        const C all = wave_max(best);
+        if (!(all > kOut))
+            break;
+        near |= r > 0 && too_near(last, all, 0x1p-18f);
+        last = all;
+        if (r == topk)
+            break;
+        const int win = __ffsll((unsigned long long)__ballot(best == all)) - 1;
+        int at = 0;
+        float value = l[0];
+#pragma unroll
+        for (int j = EPL - 1; j >= 0; --j)
+            if (c[j] == all) {
+                at = j;
+                value = l[j];
+            }
+        const int won = __builtin_amdgcn_readlane(at, win);
+        const float picked = lane_value(value, win);
+        if (lane == r) {
+            mine = win * EPL + won;
+            logit_of_mine = picked;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            c[j] = lane == win && j == won ? kOut : c[j];
+    }
+    return near;
+}
+
+template <class T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Run { T v[N]; };
 
 template <class T, int EPL, bool SOFTMAX>
 __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
 {
-    // the groups' stage reads every c of the token: one row per wave
-    __shared__ double s_c[kWaves][64 * EPL];
+    __shared__ double s_row[kWaves][64 * EPL];      // one token's scores per wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int tok = blockIdx.x * kWaves + wave;
     if (tok >= a.T)
         return;                                     // waves share nothing: no barrier below
     const T *row = static_cast<const T *>(a.logits) + tok * a.stride;
     const int e0 = lane * EPL;
-    float l[EPL];
-    float top = -INFINITY;
+    float l[EPL], b[EPL];
+    if (e0 + EPL <= a.E) {
+        const Run<T, EPL> t = *reinterpret_cast<const Run<T, EPL> *>(row + e0);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        l[j] = e0 + j < a.E ? logit(row[e0 + j]) : -INFINITY;
-        l[j] = l[j] > -INFINITY ? (l[j] > FLT_MAX ? FLT_MAX : l[j]) : -INFINITY;
-        top = l[j] > top ? l[j] : top;
-    }
-    uint64_t key[EPL];
-    const bool by_score = a.bias != nullptr || a.groups > 1;
-    double sum = 1.0;
-    if (SOFTMAX) {
+        for (int j = 0; j < EPL; ++j) {
+            l[j] = to_float(t.v[j]);
+            b[j] = 0.f;
+        }
+        if (a.bias) {
+            const Run<float, EPL> u = *reinterpret_cast<const Run<float, EPL> *>(a.bias + e0);
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const float o = __shfl_xor(top, m);
-            top = o > top ? o : top;
+            for (int j = 0; j < EPL; ++j)
+                b[j] = u.v[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            l[j] = e0 + j < a.E ? to_float(row[e0 + j]) : -INFINITY;
+            b[j] = a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.f;
         }
     }
-    if (by_score || (SOFTMAX && !a.renormalize)) {
-        double p[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)                   // NaN counts as out
+        l[j] = l[j] > -INFINITY ? (l[j] > FLT_MAX ? FLT_MAX : l[j]) : -INFINITY;
+    float top = 0.f;
+    if (SOFTMAX)
+        top = wave_max(top_of<float, EPL>(l));
+    int mine = -1;
+    float picked = 0.f;
+    double sum = 1.0;                               // softmax's own, where it does not cancel
+    // scores of type C, groups, picking; true: two were too near to tell apart
+    auto by_score = [&](auto zero) {
+        using C = decltype(zero);
+        C c[EPL], part = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            c[j] = l[j] > -INFINITY ? score_of<SOFTMAX>(l[j], top, zero) : (C)0;
+            part += c[j];
+        }
+        if (SOFTMAX) {
+            const C all = wave_sum(part);
+            sum = (double)all;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                c[j] = c[j] / all;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const C v = c[j] + (C)b[j];
+            c[j] = l[j] > -INFINITY && v > -(C)INFINITY ? v : -(C)INFINITY;
+        }
+        bool near = false;
+        if (a.groups > 1)
+            near = keep_groups<C, EPL>(c, a, lane, reinterpret_cast<C *>(s_row[wave]));
+        return pick<C, EPL>(c, l, a.topk, sizeof(C) == 4, lane, mine, picked) || near;
+    };
+    if (a.bias || a.groups > 1) {
+        if (by_score(0.f))
+            by_score(0.0);
+    } else {
+        float c[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            c[j] = l[j];
+        pick<float, EPL>(c, l, a.topk, false, lane, mine, picked);
+    }
+    if (SOFTMAX && !a.renormalize) {
         double part = 0.0;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            p[j] = l[j] > -INFINITY ? score_of<SOFTMAX>(l[j], top) : 0.0;
-            part += p[j];
-        }
-        if (SOFTMAX)
-            sum = wave_sum(part);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            double c = SOFTMAX ? p[j] / sum : p[j];
-            if (a.bias && e0 + j < a.E)
-                c += (double)a.bias[e0 + j];
-            p[j] = l[j] > -INFINITY ? c : -(double)INFINITY;
-            key[j] = key_of(p[j]);
-        }
-        if (a.groups > 1) {
-            const int per = a.E / a.groups;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                s_c[wave][e0 + j] = key[j] ? p[j] : -(double)INFINITY;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            // lane g: the two largest of group g
-            double one = -(double)INFINITY, two = -(double)INFINITY;
-            if (lane < a.groups)
-                for (int i = 0; i < per; ++i) {
-                    const double c = s_c[wave][lane * per + i];
-                    two = c > one ? one : (c > two ? c : two);
-                    one = c > one ? c : one;
-                }
-            const double score = two > -(double)INFINITY ? one + two : one;
-            int ahead = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const double o = __shfl(score, g);
-                ahead += o > score || (o == score && g < lane) ? 1 : 0;
-            }
-            const uint64_t keep = __ballot(lane < a.groups && ahead < a.topk_groups);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (e0 + j < a.E && !((keep >> ((e0 + j) / per)) & 1))
-                    key[j] = 0;
-        }
-    }
-    if (!by_score) {
-#pragma unroll
         for (int j = 0; j < EPL; ++j)
-            key[j] = key_of((double)l[j]);
+            part += l[j] > -INFINITY ? score_of<SOFTMAX>(l[j], top, 0.0) : 0.0;
+        sum = wave_sum(part);
     }
-    // lane r keeps the r-th picked expert
-    int mine = -1;
-    for (int r = 0; r < a.topk; ++r) {
-        uint64_t best = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            best = key[j] > best ? key[j] : best;
-        const uint64_t all = wave_max(best);
-        if (all == 0)
-            break;
-        const int win = __ffsll((unsigned long long)__ballot(best == all)) - 1;
-        int at = 0;
-#pragma unroll
-        for (int j = EPL - 1; j >= 0; --j)
-            at = key[j] == all ? j : at;
-        at = __builtin_amdgcn_readlane(at, win);
-        if (lane == r)
-            mine = win * EPL + at;
-        if (lane == win) {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                key[j] = j == at ? 0 : key[j];
-        }
-    }
-    double p = 0.0;
-    if (mine >= 0) {
-        float x = logit(row[mine]);
-        x = x > FLT_MAX ? FLT_MAX : x;
-        p = score_of<SOFTMAX>(x, top);
-    }
-    // the softmax's own sum cancels when the weights are renormalised
-    double w = p / (a.renormalize ? wave_sum(p) : sum) * (double)a.scale;
-    if (!(p > 0.0))
-        w = 0.0;
+    const double p = mine >= 0 ? score_of<SOFTMAX>(picked, top, 0.0) : 0.0;
+    if (a.renormalize)
+        sum = wave_sum(p);
     if (lane < a.topk) {
         const long long o = (long long)tok * a.topk + lane;
         a.ids[o] = mine;
-        a.weights[o] = (float)w;
+        a.weights[o] = p > 0.0 ? (float)(p / sum * (double)a.scale) : 0.f;
     }
 }
 
@@ -226,9 +316,9 @@ hipError_t launch_route_topk(const RouteArgs &a, int dtype, int score, hipStream
 {
     const bool softmax = score == MOE_WNA16_SOFTMAX;
     if (dtype == MOE_WNA16_BF16)
-        softmax ? launch_epl<RBf16, true>(a, stream) : launch_epl<RBf16, false>(a, stream);
+        softmax ? launch_epl<Bf16, true>(a, stream) : launch_epl<Bf16, false>(a, stream);
     else if (dtype == MOE_WNA16_FP16)
-        softmax ? launch_epl<RFp16, true>(a, stream) : launch_epl<RFp16, false>(a, stream);
+        softmax ? launch_epl<Fp16, true>(a, stream) : launch_epl<Fp16, false>(a, stream);
     else
         softmax ? launch_epl<float, true>(a, stream) : launch_epl<float, false>(a, stream);
     return hipGetLastError();

@@ -1,0 +1,104 @@
+// Element types and wave-wide reductions shared by the operators' kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace wna16 {
+
+namespace {
+
+struct Bf16 { uint16_t u; };
+struct Fp16 { uint16_t u; };
+
+__device__ __forceinline__ float to_float(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
+__device__ __forceinline__ float to_float(Fp16 v)
+{
+    return (float)__builtin_bit_cast(_Float16, v.u);
+}
+__device__ __forceinline__ float to_float(float v) { return v; }
+
+// Rounded to nearest even.
+template <class T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ Bf16 from_float<Bf16>(float v)
+{
+    return Bf16{__builtin_bit_cast(uint16_t, (__bf16)v)};
+}
+template <> __device__ __forceinline__ Fp16 from_float<Fp16>(float v)
+{
+    return Fp16{__builtin_bit_cast(uint16_t, (_Float16)v)};
+}
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+
+// Lane permutes without LDS (DPP).  The steps kXor1, kXor2, kHalfMirror,
+// kMirror reduce a row of 16 lanes: after each, the lanes of a block of 2, 4, 8,
+// 16 hold the same value, so a mirror serves where an exchange of halves would.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v)
+{
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __int_as_float(dpp<CTRL>(__float_as_int(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t l = dpp<CTRL>((uint32_t)b), h = dpp<CTRL>((uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+
+__device__ __forceinline__ int lane_value(int v, int lane)
+{
+    return __builtin_amdgcn_readlane(v, lane);
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane)
+{
+    return (uint32_t)lane_value((int)v, lane);
+}
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __int_as_float(lane_value(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t l = lane_value((uint32_t)b, lane), h = lane_value((uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+
+// Over the wave, the same on every lane.  All 64 lanes must be active.
+template <class C>
+__device__ __forceinline__ C wave_max(C v)
+{
+    v = larger(v, dpp<kXor1>(v));
+    v = larger(v, dpp<kXor2>(v));
+    v = larger(v, dpp<kHalfMirror>(v));
+    v = larger(v, dpp<kMirror>(v));
+    return larger(larger(lane_value(v, 0), lane_value(v, 16)),
+                  larger(lane_value(v, 32), lane_value(v, 48)));
+}
+template <class C>
+__device__ __forceinline__ C wave_sum(C v)
+{
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
+    v += dpp<kHalfMirror>(v);
+    v += dpp<kMirror>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+}  // namespace
+
+}  // namespace wna16
