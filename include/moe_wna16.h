@@ -398,7 +398,7 @@ typedef enum {
  *   q_out        [T, H] int8, rows q_stride apart, or NULL; with it
  *   scale_out    [T] float32
  * At least one of y_out and q_out.  Tensors aligned to their element size.
- * T >= 0 (T = 0: no launch), 1 <= H <= 65536, strides >= H, eps >= 0 finite.
+ * T >= 0 (T = 0: no launch), 1 <= H <= 32768, strides >= H, eps >= 0 finite.
  * A row with a NaN or infinity in v gets zero codes and a NaN scale; a row
  * with m < 2^-100 gets zero codes and scale 0.
  */
@@ -466,7 +466,7 @@ int moe_wna16_gemm_w8a8(const int8_t *a, const float *a_scale, const int8_t *w,
  *
  *   gu     [T, 2I] of dtype, rows gu_stride apart
  *   q_out  [T, I] int8, rows q_stride apart;  scale_out [T] float32
- * T >= 0, 1 <= I <= 65536, strides >= the row's length; alpha, beta, clamp as
+ * T >= 0, 1 <= I <= 32768, strides >= the row's length; alpha, beta, clamp as
  * in moe_wna16_forward.  Non-finite and vanishing rows as in
  * moe_wna16_add_rmsnorm.
  */

@@ -51,7 +51,7 @@ def test_valid_arguments_reach_the_device_check(name):
     ("norm", dict(eps=-1e-6), Bd.EINVAL), ("norm", dict(eps=INF), Bd.EINVAL),
     ("norm", dict(xs=63), Bd.EINVAL), ("norm", dict(rs=63), Bd.EINVAL), ("norm", dict(qs=1), Bd.EINVAL),
     ("norm", dict(rs=0, residual=None), None), ("norm", dict(qs=0, q=None), None),
-    ("norm", dict(H=65537, xs=65537, rs=65537, qs=65537), Bd.EUNSUPPORTED),
+    ("norm", dict(H=32769, xs=32769, rs=32769, qs=32769), Bd.EUNSUPPORTED),
     ("norm", dict(x=0), Bd.EINVAL), ("norm", dict(weight=0), Bd.EINVAL),
     ("norm", dict(y=0, q=0), Bd.EINVAL), ("norm", dict(s=0), Bd.EINVAL),
     ("norm", dict(q=0, s=0), None), ("norm", dict(ro=0), None), ("norm", dict(y=0), None),
@@ -85,7 +85,7 @@ def test_valid_arguments_reach_the_device_check(name):
     ("swiglu", dict(qs=63), Bd.EINVAL), ("swiglu", dict(alpha=NAN), Bd.EINVAL),
     ("swiglu", dict(beta=INF), Bd.EINVAL), ("swiglu", dict(clamp=0.0), Bd.EINVAL),
     ("swiglu", dict(clamp=NAN), Bd.EINVAL), ("swiglu", dict(clamp=-1.0), Bd.EINVAL),
-    ("swiglu", dict(I=65537, ld=131074, qs=65537), Bd.EUNSUPPORTED),
+    ("swiglu", dict(I=32769, ld=65538, qs=32769), Bd.EUNSUPPORTED),
     ("swiglu", dict(gu=0), Bd.EINVAL), ("swiglu", dict(q=0), Bd.EINVAL), ("swiglu", dict(s=0), Bd.EINVAL),
     ("swiglu", dict(gu=P + 1), Bd.EALIGN), ("swiglu", dict(gu=P + 2), None),
     ("swiglu", dict(s=P + 1), Bd.EALIGN),

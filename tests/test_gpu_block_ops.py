@@ -64,7 +64,7 @@ def check_norm(x, r, w, eps, got, quant=True):
 @pytest.mark.parametrize("dt", [BF, HF, FF])
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 7), (2, 8), (3, 130), (4, 512), (5, 513), (4, 1000),
                                  (3, 2047), (4, 4096), (2, 5120), (3, 8191), (2, 16384), (2, 20001),
-                                 (2, 32768), (1, 65535), (2, 65536), (1031, 96)])
+                                 (2, 32767), (2, 32768), (1031, 96)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm(dev, dt, T, H, residual):
     g = gen("norm", T, H, residual)
@@ -162,7 +162,7 @@ def check_swiglu(gu, alpha, beta, clamp, q, s):
 
 @pytest.mark.parametrize("dt", [BF, HF, FF])
 @pytest.mark.parametrize("T,I", [(1, 1), (2, 9), (3, 128), (4, 513), (5, 1000), (4, 2048), (2, 4097),
-                                 (2, 16384), (1, 65536), (999, 64)])
+                                 (2, 16384), (1, 32768), (999, 64)])
 @pytest.mark.parametrize("alpha,beta,clamp", [(1.0, 0.0, None), (1.702, 1.0, 7.0)])
 def test_swiglu(dev, dt, T, I, alpha, beta, clamp):
     gu = (4 * torch.randn(T, 2 * I, generator=gen("sw", T, I))).to(dt)

@@ -293,10 +293,8 @@ hipError_t with_shape(int n, F &&f)
         f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     else if (chunks <= 2048)
         f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-    else if (chunks <= 4096)
-        f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
     else
-        f(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
+        f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
     return hipGetLastError();
 }
 

@@ -23,7 +23,7 @@ struct NormArgs {
 };
 // dtype: moe_wna16_dtype of x, residual, weight, residual_out and y.
 hipError_t launch_add_rmsnorm(const NormArgs &a, int dtype, hipStream_t stream);
-constexpr int kMaxRow = 65536;                  // longest row of the row kernels
+constexpr int kMaxRow = 32768;                  // longest row of the row kernels
 
 struct SwigluArgs {
     const void *gu;                             // [T] rows of 2I: gate, then up
@@ -40,6 +40,7 @@ struct RouteArgs {
     const float *bias;                          // [E] or null
     long long stride;
     int T, E, topk, groups, topk_groups, renormalize;
+    int per_group, span;                        // set by the launch
     float scale;
     int32_t *ids;                               // [T, topk]
     float *weights;                             // [T, topk]

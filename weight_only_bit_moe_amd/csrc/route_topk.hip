@@ -41,7 +41,27 @@ namespace {
 
 constexpr int kWaves = 4;   // tokens per workgroup
 
-// exp(l - top) or sigmoid(l)
+// Order-preserving integers of the values above -inf; 0 for -inf (out).
+__device__ __forceinline__ uint32_t key_of(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.f);    // -0 and +0 are equal
+    return v > -INFINITY ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t k)
+{
+    return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t key_of(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
+    return v > -(double)INFINITY ? b ^ ((uint64_t)((int64_t)b >> 63) | 1ull << 63) : 0ull;
+}
+__device__ __forceinline__ double value_of(uint64_t k)
+{
+    return __builtin_bit_cast(double, k >> 63 ? k ^ 1ull << 63 : ~k);
+}
+
+// exp(l - top) or sigmoid(l), for picking
 template <bool SOFTMAX>
 __device__ __forceinline__ double score_of(float l, float top, double)
 {
@@ -60,6 +80,40 @@ __device__ __forceinline__ float score_of(float l, float top, float)
         return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l * -kLog2e));
 }
 
+// The weights' arithmetic: good to about 2^-36, so that only the rounding to
+// FP32 shows, at a fraction of the library functions' instructions.
+__device__ __forceinline__ double reciprocal(double v)
+{
+    const double r = __builtin_amdgcn_rcp(v);
+    return __builtin_fma(__builtin_fma(-v, r, 1.0), r, r);      // one Newton step
+}
+__device__ __forceinline__ double exp_short(double x)
+{
+    // exp(x) = 2^n exp(r), |r| <= ln(2) / 2; Taylor to r^9 leaves r^10 / 10! < 2^-36
+    x = x < -1000.0 ? -1000.0 : x;                              // 0 either way
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(-n, 0.6931471805599453, x);
+    double p = 1.0 / 362880;
+    p = __builtin_fma(p, r, 1.0 / 40320);
+    p = __builtin_fma(p, r, 1.0 / 5040);
+    p = __builtin_fma(p, r, 1.0 / 720);
+    p = __builtin_fma(p, r, 1.0 / 120);
+    p = __builtin_fma(p, r, 1.0 / 24);
+    p = __builtin_fma(p, r, 1.0 / 6);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+template <bool SOFTMAX>
+__device__ __forceinline__ double weight_of(float l, float top)
+{
+    if constexpr (SOFTMAX)
+        return exp_short((double)l - (double)top);
+    else    // beyond 700 the exponential would overflow; the weight is 0 in FP32 from 104 on
+        return reciprocal(1.0 + exp_short(l < -700.f ? 700.0 : -(double)l));
+}
+
 // Whether two 32-bit scores may be in another order in 64 bits.  A sigmoid is
 // off by less than 4 FP32 roundings; a softmax by up to 8 of its own and 22 of
 // the sum (16 scores a lane, then 6 steps); adding the bias is one more.  So a
@@ -68,132 +122,174 @@ __device__ __forceinline__ bool too_near(float a, float b, float tolerance)
 {
     return __builtin_fabsf(a - b) <= tolerance * (1.f + __builtin_fabsf(b));
 }
-__device__ __forceinline__ bool too_near(double, double, float) { return false; }
-
-template <class C, int EPL>
-__device__ __forceinline__ C top_of(const C (&c)[EPL])
-{
-    C v = c[0];
-#pragma unroll
-    for (int j = 1; j < EPL; ++j)
-        v = larger(v, c[j]);
-    return v;
-}
 
 // Takes the experts outside the best groups out of c.  Returns whether two
-// groups were too near to tell apart.
+// groups were too near to tell apart (32 bits).
 template <class C, int EPL>
 __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int lane, C *row)
 {
     const C kOut = -(C)INFINITY;
-    const int per = a.E / a.groups, span = per / EPL;
-    bool near = false;
+    const int per = a.per_group;
+    int close = 0;                                  // groups within the error, itself included
     // a group's two largest; with one expert left (or one in all) that one
     auto total = [&](C one, C two) { return two > kOut ? one + two : one; };
     auto count = [&](C score, int mine, auto &&of) {
         int ahead = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const C o = of(g);
-            ahead += o > score || (o == score && g < mine) ? 1 : 0;
-            near |= g != mine && o > kOut && score > kOut && too_near(o, score, 0x1p-17f);
+        if constexpr (sizeof(C) == 4) {
+            // equal scores are near, so 64 bits decide them
+            const float reach = 0x1p-17f * (1.f + __builtin_fabsf(score));
+            for (int g = 0; g < a.groups; ++g) {
+                const C o = of(g);
+                ahead += o > score ? 1 : 0;
+                close += __builtin_fabsf(o - score) <= reach ? 1 : 0;
+            }
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                const C o = of(g);
+                ahead += o > score || (o == score && g < mine) ? 1 : 0;
+            }
         }
+        if (!(score > kOut && score < (C)INFINITY))
+            close = score > kOut ? 2 : 0;           // infinite scores go to 64 bits
         return ahead;
     };
-    if (span * EPL == per && (span == 2 || span == 4 || span == 8 || span == 16)) {
-        // groups are whole runs of lanes: merge the lanes' pairs by permutes
+    if (a.span > 0) {
+        // groups are whole runs of `span` lanes: merge the lanes' pairs by permutes
         C one = kOut, two = kOut;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            two = c[j] > one ? one : larger(two, c[j]);
-            one = larger(one, c[j]);
+            two = c[j] > one ? one : (c[j] > two ? c[j] : two);
+            one = c[j] > one ? c[j] : one;
         }
         auto merge = [&](C o1, C o2) {
-            two = o1 > one ? larger(one, o2) : larger(two, o1);
-            one = larger(one, o1);
+            const C low = o1 > one ? one : o1, high = o1 > one ? o2 : two;
+            two = high > low ? high : low;
+            one = o1 > one ? o1 : one;
         };
         merge(dpp<kXor1>(one), dpp<kXor1>(two));
-        if (span >= 4)
+        if (a.span >= 4)
             merge(dpp<kXor2>(one), dpp<kXor2>(two));
-        if (span >= 8)
+        if (a.span >= 8)
             merge(dpp<kHalfMirror>(one), dpp<kHalfMirror>(two));
-        if (span >= 16)
+        if (a.span >= 16)
             merge(dpp<kMirror>(one), dpp<kMirror>(two));
         const C score = total(one, two);
-        const int mine = lane / span;
-        const int ahead = count(score, mine, [&](int g) { return lane_value(score, g * span); });
-        if (ahead >= a.topk_groups) {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                c[j] = kOut;
-        }
-        near = near && mine < a.groups;
-    } else {
-        // any other shape: lane g reads group g's scores
-        const int e0 = lane * EPL;
+        const int shift = __ffs(a.span) - 1;
+        const int ahead = count(score, lane >> shift,
+                                [&](int g) { return lane_value(score, g << shift); });
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            row[e0 + j] = c[j];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        C one = kOut, two = kOut;
-        if (lane < a.groups)
-            for (int i = 0; i < per; ++i) {
-                const C v = row[lane * per + i];
-                two = v > one ? one : larger(two, v);
-                one = larger(one, v);
-            }
-        const C score = total(one, two);
-        const int ahead = count(score, lane, [&](int g) { return lane_value(score, g); });
-        const uint64_t keep = __ballot(lane < a.groups && ahead < a.topk_groups);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (e0 + j < a.E && !((keep >> ((e0 + j) / per)) & 1))
-                c[j] = kOut;
-        near = near && lane < a.groups;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+            c[j] = ahead >= a.topk_groups ? kOut : c[j];
+        return __ballot(close > 1) != 0;            // lanes past the experts have no score
     }
-    return __ballot(near) != 0;
+    // any other shape: lane g reads group g's scores
+    const int e0 = lane * EPL;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        row[e0 + j] = c[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    C one = kOut, two = kOut;
+    if (lane < a.groups)
+        for (int i = 0; i < per; ++i) {
+            const C v = row[lane * per + i];
+            two = v > one ? one : (v > two ? v : two);
+            one = v > one ? v : one;
+        }
+    const C score = total(one, two);
+    const int ahead = count(score, lane, [&](int g) { return lane_value(score, g); });
+    const uint64_t keep = __ballot(lane < a.groups && ahead < a.topk_groups);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        if (e0 + j < a.E && !((keep >> ((e0 + j) / per)) & 1))
+            c[j] = kOut;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return __ballot(close > 1) != 0;
 }
 
-// Picks the topk largest of c: lane r gets the r-th pick and its logit.
-// Returns whether two that had to be told apart were too near.
-template <class C, int EPL>
-__device__ __forceinline__ bool pick(C (&c)[EPL], const float (&l)[EPL], int topk, bool check,
-                                     int lane, int &mine, float &logit_of_mine)
+// One lane's experts: keys, slots and logits, largest key first (ties: lower slot).
+template <class K, int EPL>
+struct Sorted {
+    K key[EPL];
+    int slot[EPL];
+    float l[EPL];
+
+    __device__ __forceinline__ void order(int i, int j)
+    {
+        const bool swap = key[j] > key[i] || (key[j] == key[i] && slot[j] < slot[i]);
+        const K k = key[i];
+        const int s = slot[i];
+        const float x = l[i];
+        key[i] = swap ? key[j] : k;
+        key[j] = swap ? k : key[j];
+        slot[i] = swap ? slot[j] : s;
+        slot[j] = swap ? s : slot[j];
+        l[i] = swap ? l[j] : x;
+        l[j] = swap ? x : l[j];
+    }
+    // Batcher's odd-even merge sort
+    __device__ __forceinline__ void sort()
+    {
+#pragma unroll
+        for (int p = 1; p < EPL; p <<= 1)
+#pragma unroll
+            for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+                for (int j = k % p; j + k < EPL; j += 2 * k)
+#pragma unroll
+                    for (int i = 0; i < k; ++i)
+                        if (i + j + k < EPL && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+                            order(i + j, i + j + k);
+    }
+    __device__ __forceinline__ void drop_first(bool me)
+    {
+#pragma unroll
+        for (int j = 0; j + 1 < EPL; ++j) {
+            key[j] = me ? key[j + 1] : key[j];
+            slot[j] = me ? slot[j + 1] : slot[j];
+            l[j] = me ? l[j + 1] : l[j];
+        }
+        key[EPL - 1] = me ? (K)0 : key[EPL - 1];
+    }
+};
+
+// Picks the topk largest of c: lane r gets the r-th pick and its logit.  With
+// CHECK (32-bit scores) returns whether two that had to be told apart were too
+// near; one more round shows the first expert left out.
+template <bool CHECK, class C, int EPL>
+__device__ __forceinline__ bool pick(const C (&c)[EPL], const float (&l)[EPL], int topk, int lane,
+                                     int &mine, float &picked)
 {
-    const C kOut = -(C)INFINITY;
+    using K = decltype(key_of(c[0]));
+    Sorted<K, EPL> s;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        s.key[j] = key_of(c[j]);
+        s.slot[j] = j;
+        s.l[j] = l[j];
+    }
+    s.sort();
     mine = -1;
     bool near = false;
-    C last = (C)INFINITY;
-    const int rounds = check ? topk + 1 : topk;     // one more: the first left out
+    K last = 0;
+    const int rounds = CHECK ? topk + 1 : topk;
     for (int r = 0; r < rounds; ++r) {
-        const C best = top_of<C, EPL>(c);
-        const C all = wave_max(best);
-        if (!(all > kOut))
+        const K all = wave_max(s.key[0]);
+        if (all == 0)
             break;
-        near |= r > 0 && too_near(last, all, 0x1p-18f);
+        if constexpr (CHECK)
+            near |= r > 0 && too_near(value_of(last), value_of(all), 0x1p-18f);
         last = all;
-        if (r == topk)
-            break;
-        const int win = __ffsll((unsigned long long)__ballot(best == all)) - 1;
-        int at = 0;
-        float value = l[0];
-#pragma unroll
-        for (int j = EPL - 1; j >= 0; --j)
-            if (c[j] == all) {
-                at = j;
-                value = l[j];
-            }
-        const int won = __builtin_amdgcn_readlane(at, win);
-        const float picked = lane_value(value, win);
-        if (lane == r) {
-            mine = win * EPL + won;
-            logit_of_mine = picked;
+        const uint64_t who = __ballot(s.key[0] == all);
+        const int win = __builtin_ctzll(who);
+        const int id = win * EPL + lane_value(s.slot[0], win);
+        const float x = lane_value(s.l[0], win);
+        if (r < topk) {
+            mine = lane == r ? id : mine;
+            picked = lane == r ? x : picked;
         }
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            c[j] = lane == win && j == won ? kOut : c[j];
+        s.drop_first(lane == win);
     }
     return near;
 }
@@ -204,7 +300,8 @@ template <class T, int EPL, bool SOFTMAX>
 __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
 {
     __shared__ double s_row[kWaves][64 * EPL];      // one token's scores per wave
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tok = blockIdx.x * kWaves + wave;
     if (tok >= a.T)
         return;                                     // waves share nothing: no barrier below
@@ -232,26 +329,32 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
         }
     }
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)                   // NaN counts as out
-        l[j] = l[j] > -INFINITY ? (l[j] > FLT_MAX ? FLT_MAX : l[j]) : -INFINITY;
+    for (int j = 0; j < EPL; ++j) {                 // NaN counts as out
+        const float x = __builtin_fminf(l[j], FLT_MAX);
+        l[j] = l[j] > -INFINITY ? x : -INFINITY;
+    }
     float top = 0.f;
-    if (SOFTMAX)
-        top = wave_max(top_of<float, EPL>(l));
+    if (SOFTMAX) {
+        float m = l[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j)
+            m = larger(m, l[j]);
+        top = wave_max(m);
+    }
     int mine = -1;
     float picked = 0.f;
-    double sum = 1.0;                               // softmax's own, where it does not cancel
     // scores of type C, groups, picking; true: two were too near to tell apart
     auto by_score = [&](auto zero) {
         using C = decltype(zero);
         C c[EPL], part = 0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            c[j] = l[j] > -INFINITY ? score_of<SOFTMAX>(l[j], top, zero) : (C)0;
+            c[j] = score_of<SOFTMAX>(l[j], top, zero);
+            c[j] = l[j] > -INFINITY ? c[j] : (C)0;
             part += c[j];
         }
         if (SOFTMAX) {
             const C all = wave_sum(part);
-            sum = (double)all;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 c[j] = c[j] / all;
@@ -264,32 +367,31 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
         bool near = false;
         if (a.groups > 1)
             near = keep_groups<C, EPL>(c, a, lane, reinterpret_cast<C *>(s_row[wave]));
-        return pick<C, EPL>(c, l, a.topk, sizeof(C) == 4, lane, mine, picked) || near;
+        return pick<sizeof(C) == 4, C, EPL>(c, l, a.topk, lane, mine, picked) || near;
     };
     if (a.bias || a.groups > 1) {
         if (by_score(0.f))
             by_score(0.0);
     } else {
-        float c[EPL];
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            c[j] = l[j];
-        pick<float, EPL>(c, l, a.topk, false, lane, mine, picked);
+        pick<false, float, EPL>(l, l, a.topk, lane, mine, picked);
     }
-    if (SOFTMAX && !a.renormalize) {
+    double sum = 1.0;
+    if (SOFTMAX && !a.renormalize) {                // softmax's own sum does not cancel
         double part = 0.0;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            part += l[j] > -INFINITY ? score_of<SOFTMAX>(l[j], top, 0.0) : 0.0;
+            part += l[j] > -INFINITY ? weight_of<SOFTMAX>(l[j], top) : 0.0;
         sum = wave_sum(part);
     }
-    const double p = mine >= 0 ? score_of<SOFTMAX>(picked, top, 0.0) : 0.0;
+    const double p = mine >= 0 ? weight_of<SOFTMAX>(picked, top) : 0.0;
     if (a.renormalize)
         sum = wave_sum(p);
     if (lane < a.topk) {
         const long long o = (long long)tok * a.topk + lane;
         a.ids[o] = mine;
-        a.weights[o] = p > 0.0 ? (float)(p / sum * (double)a.scale) : 0.f;
+        // sums so small that their reciprocal would overflow weigh nothing in FP32 either
+        const double w = sum > 0x1p-1000 ? p * reciprocal(sum) : 0.0;
+        a.weights[o] = (float)(w * (double)a.scale);
     }
 }
 
@@ -297,17 +399,28 @@ template <class T, bool SOFTMAX>
 void launch_epl(const RouteArgs &a, hipStream_t stream)
 {
     const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);
+    auto go = [&](auto n) {
+        constexpr int EPL = decltype(n)::value;
+        RouteArgs b = a;
+        b.per_group = a.E / a.groups;
+        // groups that are whole power-of-two runs of at most 16 lanes merge by permutes
+        const int span = b.per_group / EPL;
+        b.span = span * EPL == b.per_group && span >= 2 && span <= 16 && (span & (span - 1)) == 0
+                     ? span
+                     : 0;
+        route_topk_kernel<T, EPL, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(b);
+    };
     const int epl = (a.E + 63) / 64;
     if (epl <= 1)
-        route_topk_kernel<T, 1, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(a);
+        go(std::integral_constant<int, 1>{});
     else if (epl <= 2)
-        route_topk_kernel<T, 2, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(a);
+        go(std::integral_constant<int, 2>{});
     else if (epl <= 4)
-        route_topk_kernel<T, 4, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(a);
+        go(std::integral_constant<int, 4>{});
     else if (epl <= 8)
-        route_topk_kernel<T, 8, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(a);
+        go(std::integral_constant<int, 8>{});
     else
-        route_topk_kernel<T, 16, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(a);
+        go(std::integral_constant<int, 16>{});
 }
 
 }  // namespace

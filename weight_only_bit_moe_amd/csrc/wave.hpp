@@ -38,7 +38,7 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v)
 {
-    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) { return (uint32_t)dpp<CTRL>((int)v); }
@@ -48,11 +48,14 @@ __device__ __forceinline__ float dpp(float v)
     return __int_as_float(dpp<CTRL>(__float_as_int(v)));
 }
 template <int CTRL>
+__device__ __forceinline__ uint64_t dpp(uint64_t v)
+{
+    return (uint64_t)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
+}
+template <int CTRL>
 __device__ __forceinline__ double dpp(double v)
 {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t l = dpp<CTRL>((uint32_t)b), h = dpp<CTRL>((uint32_t)(b >> 32));
-    return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+    return __builtin_bit_cast(double, dpp<CTRL>(__builtin_bit_cast(uint64_t, v)));
 }
 
 __device__ __forceinline__ int lane_value(int v, int lane)
@@ -67,14 +70,17 @@ __device__ __forceinline__ float lane_value(float v, int lane)
 {
     return __int_as_float(lane_value(__float_as_int(v), lane));
 }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane)
+{
+    return (uint64_t)lane_value((uint32_t)(v >> 32), lane) << 32 | lane_value((uint32_t)v, lane);
+}
 __device__ __forceinline__ double lane_value(double v, int lane)
 {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t l = lane_value((uint32_t)b, lane), h = lane_value((uint32_t)(b >> 32), lane);
-    return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+    return __builtin_bit_cast(double, lane_value(__builtin_bit_cast(uint64_t, v), lane));
 }
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 
