@@ -15,16 +15,16 @@
 // Which of two nearly equal c is ahead decides which expert runs, so the order
 // is that of 64-bit scores: two experts swap only if they agree to about 2^-52.
 // Most tokens need no 64-bit score for it.  The scores are first taken in
-// 32 bits, where they are off by less than 2^-19 (1 + |c|), and the token keeps
-// that order if every comparison that mattered was wider than the two errors:
+// 32 bits, and the token keeps that order if every comparison that mattered was
+// wider than the two errors (kScoreError below):
 // consecutive picks, the last pick and the first expert left out, and any two
 // groups.  Otherwise the wave repeats the picking in 64 bits.  Without bias and
 // groups the order of c is the order of the logits, which is exact in 32 bits.
 // The weights of the picked experts are always computed in 64 bits.
 //
-// One wave owns a token; lane i holds experts [i*EPL, (i+1)*EPL).  Picking is
-// rounds of a wave-wide maximum (DPP, no LDS), each taking the lowest lane and
-// slot that hold the maximum.  With one token the time is the chain of memory
+// One wave owns a token, each lane EPL of its experts, sorted once.  Picking is
+// rounds of a wave-wide maximum over the lanes' largest (DPP, no LDS); the lane
+// that held it moves on to its next.  With one token the time is the chain of memory
 // round trips and reductions; with many it is the VALU instructions per token.
 #include <hip/hip_runtime.h>
 
@@ -114,10 +114,14 @@ __device__ __forceinline__ double weight_of(float l, float top)
         return reciprocal(1.0 + exp_short(l < -700.f ? 700.0 : -(double)l));
 }
 
-// Whether two 32-bit scores may be in another order in 64 bits.  A sigmoid is
-// off by less than 4 FP32 roundings; a softmax by up to 8 of its own and 22 of
-// the sum (16 scores a lane, then 6 steps); adding the bias is one more.  So a
-// score is off by less than 2^-19 (1 + |c|), a group's sum of two by twice that.
+// Errors of a 32-bit score, in FP32 roundings of 1 + |c|: a sigmoid is off by
+// less than 4, a softmax by up to 8 of its own and 22 of the sum (16 scores a
+// lane, then 6 steps); adding the bias is one more; a key that gives its lowest
+// log2(EPL) bits to the slot is off by EPL.  Two scores may be in another order
+// in 64 bits if they differ by less than both errors, two groups' sums of two
+// scores if they differ by less than four.
+template <bool SOFTMAX> constexpr float kScoreError = (SOFTMAX ? 31 : 5) * 0x1p-24f;
+
 __device__ __forceinline__ bool too_near(float a, float b, float tolerance)
 {
     return __builtin_fabsf(a - b) <= tolerance * (1.f + __builtin_fabsf(b));
@@ -125,7 +129,7 @@ __device__ __forceinline__ bool too_near(float a, float b, float tolerance)
 
 // Takes the experts outside the best groups out of c.  Returns whether two
 // groups were too near to tell apart (32 bits).
-template <class C, int EPL>
+template <class C, int EPL, bool SOFTMAX>
 __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int lane, C *row)
 {
     const C kOut = -(C)INFINITY;
@@ -137,7 +141,7 @@ __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int
         int ahead = 0;
         if constexpr (sizeof(C) == 4) {
             // equal scores are near, so 64 bits decide them
-            const float reach = 0x1p-17f * (1.f + __builtin_fabsf(score));
+            const float reach = 4 * kScoreError<SOFTMAX> * (1.f + __builtin_fabsf(score));
             for (int g = 0; g < a.groups; ++g) {
                 const C o = of(g);
                 ahead += o > score ? 1 : 0;
@@ -208,107 +212,123 @@ __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int
     return __ballot(close > 1) != 0;
 }
 
-// One lane's experts: keys, slots and logits, largest key first (ties: lower slot).
-template <class K, int EPL>
-struct Sorted {
-    K key[EPL];
-    int slot[EPL];
-    float l[EPL];
+// Batcher's odd-even merge sort of n values by order(i, j), i < j.
+template <int N, class F>
+__device__ __forceinline__ void sort_network(F &&order)
+{
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+                        order(i + j, i + j + k);
+}
 
-    __device__ __forceinline__ void order(int i, int j)
-    {
+// Picks by packed keys, largest first: lane r's `mine` is the r-th pick.
+// Distinct keys, so a lane's are sorted by min and max alone.  With EXTRA, one
+// more round shows the first expert left out.  id(key, lane) names the expert,
+// near(last, key) whether two keys in a row were too near to tell apart.
+template <bool EXTRA, class K, int EPL, class Id, class Near>
+__device__ __forceinline__ bool pick(K (&key)[EPL], int topk, int lane, int &mine, Id &&id,
+                                     Near &&near_to)
+{
+    sort_network<EPL>([&](int i, int j) {
+        const K hi = larger(key[i], key[j]), lo = key[i] > key[j] ? key[j] : key[i];
+        key[i] = hi;
+        key[j] = lo;
+    });
+    mine = -1;
+    K taken = 0, last = 0;                          // taken: lane r's the r-th picked key
+    int n = 0;
+    for (; n < topk; ++n) {
+        const K all = wave_max(key[0]);
+        if (all == 0)
+            break;
+        last = all;
+        const int win = __builtin_ctzll(__ballot(key[0] == all));
+        const int e = id(all, win);
+        mine = lane == n ? e : mine;
+        if constexpr (EXTRA)
+            taken = lane == n ? all : taken;
+        const bool me = lane == win;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const K own = key[j], next = j + 1 < EPL ? key[j + 1] : (K)0;
+            key[j] = me ? next : own;
+        }
+    }
+    if constexpr (EXTRA) {
+        const K before = (K)__shfl_up((int)taken, 1);
+        const K left = n == topk ? wave_max(key[0]) : 0;
+        return __ballot(lane > 0 && lane < n && near_to(before, taken)) != 0 ||
+               (left != 0 && near_to(last, left));
+    }
+    return false;
+}
+
+// The same by 64-bit scores, whose keys leave no room for the slot: a lane's
+// equal keys are sorted by slot, and the wave takes the lowest lane.
+template <int EPL>
+__device__ __forceinline__ void pick_exact(const double (&c)[EPL], int topk, int lane, int &mine)
+{
+    uint64_t key[EPL];
+    int slot[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        key[j] = key_of(c[j]);
+        slot[j] = j;
+    }
+    sort_network<EPL>([&](int i, int j) {
         const bool swap = key[j] > key[i] || (key[j] == key[i] && slot[j] < slot[i]);
-        const K k = key[i];
+        const uint64_t k = key[i];
         const int s = slot[i];
-        const float x = l[i];
         key[i] = swap ? key[j] : k;
         key[j] = swap ? k : key[j];
         slot[i] = swap ? slot[j] : s;
         slot[j] = swap ? s : slot[j];
-        l[i] = swap ? l[j] : x;
-        l[j] = swap ? x : l[j];
-    }
-    // Batcher's odd-even merge sort
-    __device__ __forceinline__ void sort()
-    {
-#pragma unroll
-        for (int p = 1; p < EPL; p <<= 1)
-#pragma unroll
-            for (int k = p; k >= 1; k >>= 1)
-#pragma unroll
-                for (int j = k % p; j + k < EPL; j += 2 * k)
-#pragma unroll
-                    for (int i = 0; i < k; ++i)
-                        if (i + j + k < EPL && (i + j) / (2 * p) == (i + j + k) / (2 * p))
-                            order(i + j, i + j + k);
-    }
-    __device__ __forceinline__ void drop_first(bool me)
-    {
-#pragma unroll
-        for (int j = 0; j + 1 < EPL; ++j) {
-            key[j] = me ? key[j + 1] : key[j];
-            slot[j] = me ? slot[j + 1] : slot[j];
-            l[j] = me ? l[j + 1] : l[j];
-        }
-        key[EPL - 1] = me ? (K)0 : key[EPL - 1];
-    }
-};
-
-// Picks the topk largest of c: lane r gets the r-th pick and its logit.  With
-// CHECK (32-bit scores) returns whether two that had to be told apart were too
-// near; one more round shows the first expert left out.
-template <bool CHECK, class C, int EPL>
-__device__ __forceinline__ bool pick(const C (&c)[EPL], const float (&l)[EPL], int topk, int lane,
-                                     int &mine, float &picked)
-{
-    using K = decltype(key_of(c[0]));
-    Sorted<K, EPL> s;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        s.key[j] = key_of(c[j]);
-        s.slot[j] = j;
-        s.l[j] = l[j];
-    }
-    s.sort();
+    });
     mine = -1;
-    bool near = false;
-    K last = 0;
-    const int rounds = CHECK ? topk + 1 : topk;
-    for (int r = 0; r < rounds; ++r) {
-        const K all = wave_max(s.key[0]);
+    for (int r = 0; r < topk; ++r) {
+        const uint64_t all = wave_max(key[0]);
         if (all == 0)
             break;
-        if constexpr (CHECK)
-            near |= r > 0 && too_near(value_of(last), value_of(all), 0x1p-18f);
-        last = all;
-        const uint64_t who = __ballot(s.key[0] == all);
-        const int win = __builtin_ctzll(who);
-        const int id = win * EPL + lane_value(s.slot[0], win);
-        const float x = lane_value(s.l[0], win);
-        if (r < topk) {
-            mine = lane == r ? id : mine;
-            picked = lane == r ? x : picked;
+        const int win = __builtin_ctzll(__ballot(key[0] == all));
+        const int e = win * EPL + lane_value(slot[0], win);
+        mine = lane == r ? e : mine;
+        const bool me = lane == win;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const uint64_t own = key[j], next = j + 1 < EPL ? key[j + 1] : 0ull;
+            const int here = slot[j], there = j + 1 < EPL ? slot[j + 1] : 0;
+            key[j] = me ? next : own;
+            slot[j] = me ? there : here;
         }
-        s.drop_first(lane == win);
     }
-    return near;
 }
 
 template <class T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Run { T v[N]; };
 
-template <class T, int EPL, bool SOFTMAX>
+// BY_SCORE: with a bias or groups, lane i holds experts [i*EPL, (i+1)*EPL), so
+// that groups are runs of lanes.  Otherwise it holds experts i, i + 64, ..., so
+// that the slot and then the lane order equal logits by expert.
+template <class T, int EPL, bool SOFTMAX, bool BY_SCORE>
 __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
 {
-    __shared__ double s_row[kWaves][64 * EPL];      // one token's scores per wave
+    __shared__ double s_row[kWaves][64 * EPL];      // one token's scores, then its logits
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tok = blockIdx.x * kWaves + wave;
     if (tok >= a.T)
         return;                                     // waves share nothing: no barrier below
     const T *row = static_cast<const T *>(a.logits) + tok * a.stride;
-    const int e0 = lane * EPL;
+    const int e0 = BY_SCORE ? lane * EPL : lane;
+    constexpr int kStep = BY_SCORE ? 1 : 64;
     float l[EPL], b[EPL];
-    if (e0 + EPL <= a.E) {
+    if (BY_SCORE && e0 + EPL <= a.E) {
         const Run<T, EPL> t = *reinterpret_cast<const Run<T, EPL> *>(row + e0);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
@@ -324,8 +344,9 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            l[j] = e0 + j < a.E ? to_float(row[e0 + j]) : -INFINITY;
-            b[j] = a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.f;
+            const int e = e0 + j * kStep;
+            l[j] = e < a.E ? to_float(row[e]) : -INFINITY;
+            b[j] = BY_SCORE && a.bias && e < a.E ? a.bias[e] : 0.f;
         }
     }
 #pragma unroll
@@ -342,39 +363,87 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
         top = wave_max(m);
     }
     int mine = -1;
-    float picked = 0.f;
-    // scores of type C, groups, picking; true: two were too near to tell apart
-    auto by_score = [&](auto zero) {
-        using C = decltype(zero);
-        C c[EPL], part = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            c[j] = score_of<SOFTMAX>(l[j], top, zero);
-            c[j] = l[j] > -INFINITY ? c[j] : (C)0;
-            part += c[j];
-        }
-        if (SOFTMAX) {
-            const C all = wave_sum(part);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                c[j] = c[j] / all;
-        }
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const C v = c[j] + (C)b[j];
-            c[j] = l[j] > -INFINITY && v > -(C)INFINITY ? v : -(C)INFINITY;
-        }
-        bool near = false;
-        if (a.groups > 1)
-            near = keep_groups<C, EPL>(c, a, lane, reinterpret_cast<C *>(s_row[wave]));
-        return pick<sizeof(C) == 4, C, EPL>(c, l, a.topk, lane, mine, picked) || near;
+    // A 32-bit key gives its lowest bits to the slot (a lower slot counts as
+    // more), which costs log2(EPL) of the 24 bits of a score.
+    constexpr uint32_t kSlots = EPL - 1;
+    auto packed = [&](float v, int j) {
+        const uint32_t k = key_of(v);
+        return k ? (k & ~kSlots) | (kSlots - j) : 0u;
     };
-    if (a.bias || a.groups > 1) {
-        if (by_score(0.f))
-            by_score(0.0);
+    if constexpr (BY_SCORE) {
+        auto scores = [&](auto &c, auto zero) {
+            using C = decltype(zero);
+            C part = 0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                c[j] = score_of<SOFTMAX>(l[j], top, zero);
+                c[j] = l[j] > -INFINITY ? c[j] : (C)0;
+                part += c[j];
+            }
+            if (SOFTMAX) {
+                const C all = wave_sum(part);
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    c[j] = c[j] / all;
+            }
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                const C v = c[j] + (C)b[j];
+                c[j] = l[j] > -INFINITY && v > -(C)INFINITY ? v : -(C)INFINITY;
+            }
+            return a.groups > 1 && keep_groups<C, EPL, SOFTMAX>(
+                                       c, a, lane, reinterpret_cast<C *>(s_row[wave]));
+        };
+        float c[EPL];
+        bool near = scores(c, 0.f);
+        uint32_t key[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            key[j] = packed(c[j], j);
+        near |= pick<true>(
+            key, a.topk, lane, mine,
+            [&](uint32_t k, int win) { return win * EPL + (int)(kSlots - (k & kSlots)); },
+            [&](uint32_t last, uint32_t k) {
+                return too_near(value_of(last), value_of(k),
+                                2 * (kScoreError<SOFTMAX> + EPL * 0x1p-24f));
+            });
+        if (near) {
+            double d[EPL];
+            scores(d, 0.0);
+            pick_exact<EPL>(d, a.topk, lane, mine);
+        }
     } else {
-        pick<false, float, EPL>(l, l, a.topk, lane, mine, picked);
+        uint32_t key[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            key[j] = packed(l[j], j);
+        // 16-bit logits keep all their bits; FP32 logits that differ in the lost ones only
+        // (or not at all) are picked again by 64-bit keys with all bits and the expert
+        const bool near = pick<sizeof(T) == 4>(
+            key, a.topk, lane, mine,
+            [&](uint32_t k, int win) { return win + 64 * (int)(kSlots - (k & kSlots)); },
+            [&](uint32_t last, uint32_t k) { return sizeof(T) == 4 && (last ^ k) <= kSlots; });
+        if (near) {
+            uint64_t full[EPL];
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                const uint32_t k = key_of(l[j]);
+                full[j] = k ? (uint64_t)k << 32 | (uint32_t)(1023 - (lane + 64 * j)) : 0ull;
+            }
+            pick<false>(
+                full, a.topk, lane, mine,
+                [&](uint64_t k, int) { return 1023 - (int)(uint32_t)k; },
+                [&](uint64_t, uint64_t) { return false; });
+        }
     }
+    // the picked experts' logits
+    float *held = reinterpret_cast<float *>(s_row[wave]);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        held[e0 + j * kStep] = l[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const float picked = mine >= 0 ? held[mine] : 0.f;
     double sum = 1.0;
     if (SOFTMAX && !a.renormalize) {                // softmax's own sum does not cancel
         double part = 0.0;
@@ -408,7 +477,10 @@ void launch_epl(const RouteArgs &a, hipStream_t stream)
         b.span = span * EPL == b.per_group && span >= 2 && span <= 16 && (span & (span - 1)) == 0
                      ? span
                      : 0;
-        route_topk_kernel<T, EPL, SOFTMAX><<<grid, 64 * kWaves, 0, stream>>>(b);
+        if (a.bias || a.groups > 1)
+            route_topk_kernel<T, EPL, SOFTMAX, true><<<grid, 64 * kWaves, 0, stream>>>(b);
+        else
+            route_topk_kernel<T, EPL, SOFTMAX, false><<<grid, 64 * kWaves, 0, stream>>>(b);
     };
     const int epl = (a.E + 63) / 64;
     if (epl <= 1)

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace wna16 {
 
 namespace {
@@ -92,6 +94,15 @@ __device__ __forceinline__ C wave_max(C v)
     v = larger(v, dpp<kXor2>(v));
     v = larger(v, dpp<kHalfMirror>(v));
     v = larger(v, dpp<kMirror>(v));
+    if constexpr (std::is_same<C, uint32_t>::value) {
+        // kept in scalar registers: what follows is then scalar too
+        uint32_t a = larger(lane_value(v, 0), lane_value(v, 16));
+        uint32_t b = larger(lane_value(v, 32), lane_value(v, 48));
+        asm("" : "+s"(a), "+s"(b));
+        uint32_t r = larger(a, b);
+        asm("" : "+s"(r));
+        return r;
+    }
     return larger(larger(lane_value(v, 0), lane_value(v, 16)),
                   larger(lane_value(v, 32), lane_value(v, 48)));
 }
