@@ -71,14 +71,166 @@ __device__ __forceinline__ v4i load_tail(const int8_t *p, int left)
     return r;
 }
 
+// LDS byte address of a __shared__ pointer.
+__device__ __forceinline__ uint32_t lds_of(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)(p);
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// Lane l's 16 bytes at base + voff land at LDS address lds + l * 16.  base and
+// lds are wave-uniform.  Inline asm, so that the compiler does not make every
+// later LDS read wait for all copies in flight; the caller waits with vmcnt.
+__device__ __forceinline__ void copy16_to_lds(const int8_t *base_in, uint32_t voff, uint32_t lds_in)
+{
+    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_in);
+    const uint64_t b = reinterpret_cast<uintptr_t>(base_in);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+    const void *base = reinterpret_cast<const void *>(((uint64_t)hi << 32) | (uint64_t)lo);
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base),
+                 "s"(lds)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Place of a row's 16-byte piece c among the 8 of its 128-byte LDS row: the 16
+// rows that one MFMA operand read touches are spread over all banks.
+__device__ __forceinline__ int place(int row, int c) { return c ^ ((row >> 1) & 7); }
+
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Sums the waves' 16-channel x MT*16-token results and writes them.
+template <int MT, int NW>
+__device__ __forceinline__ void join_waves(const GemmArgs &g, const v4i (&acc)[MT], int *part,
+                                           int n0, int t0, int out_dtype)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        *reinterpret_cast<v4i *>(part + ((wave * MT + m) * 64 + lane) * 4) = acc[m];
+    __syncthreads();
+    for (int m = wave; m < MT; m += NW) {
+        v4i sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            sum += *reinterpret_cast<const v4i *>(part + ((i * MT + m) * 64 + lane) * 4);
+        const int v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        const int t = t0 + m * 16 + (lane & 15), n = n0 + (lane >> 4) * 4;
+        if (out_dtype == MOE_WNA16_BF16)
+            emit4<Bf16>(g, t, n, v);
+        else if (out_dtype == MOE_WNA16_FP16)
+            emit4<Fp16>(g, t, n, v);
+        else
+            emit4<float>(g, t, n, v);
+    }
+}
+
 // ---------------------------------------------------------------------------
-// Few tokens, and operands that no 16-byte copy can address.  A workgroup owns
-// 16 channels and up to MT * 16 tokens; its waves split K and add their sums
-// through LDS.  Both operands go from memory to the MFMA's registers directly:
-// lane l holds 16 bytes of row l % 16 at K offset 16 * (l / 16), so a wave's
-// load covers 64 consecutive bytes of 16 rows, and the next one the rest of the
-// 128-byte lines.  Channels are the MFMA's rows, so a lane ends up with four
-// consecutive channels of one token and stores them at once.
+// Few tokens (decode): the weights are streamed once.  A workgroup owns 16
+// channels and all tokens (up to 8 * TC); its waves take the 128-byte chunks of
+// K in turn and add their sums through LDS at the end.  Each wave copies its
+// chunks into its own ring of R stages, so no barrier is needed before the
+// join.  The way through LDS is for the addresses: an MFMA wants lane l to hold
+// row l % 16, and a load in that order has every lane in another row, which the
+// address unit takes one lane a cycle; the copies take eight lanes of one row
+// in a row, four lanes a cycle.
+// ---------------------------------------------------------------------------
+template <int TC, int NW, int R>
+__global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g, int out_dtype)
+{
+    constexpr int MT = TC < 2 ? 1 : TC / 2, ROWS = 16 + 8 * TC, STAGE = ROWS * 128;
+    constexpr int COPIES = ROWS / 8, RING = NW * R * STAGE, PART = NW * MT * 1024;
+    __shared__ __attribute__((aligned(1024))) char lds[RING > PART ? RING : PART];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16;
+    char *ring = lds + wave * (R * STAGE);
+    const uint32_t ring0 = lds_of(ring);
+    // copy i brings rows [8i, 8i + 8): channels first, then tokens; rows past
+    // the end repeat the last one
+    const int crow = lane >> 3;
+    uint32_t off[COPIES];
+    int cplace[2] = {place(crow, lane & 7) * 16, place(8 + crow, lane & 7) * 16};
+    const int8_t *wbase = g.w + (long long)n0 * g.ldw;
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+        const int row = i < 2 ? i * 8 + crow : (i - 2) * 8 + crow;
+        const int last = i < 2 ? g.N - 1 - n0 : g.T - 1;
+        off[i] = (uint32_t)((row < last ? row : last) * (i < 2 ? g.ldw : g.lda)) +
+                 (uint32_t)cplace[i & 1];
+    }
+    const int chunks = (g.K + 127) / 128;
+    auto copy = [&](int c, int stage) {
+        const bool part = (c + 1) * 128 > g.K;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            uint32_t o = off[i] + (uint32_t)(c * 128);
+            // K past the end (a multiple of 16): the row's first piece is read
+            // again, and the channels' registers are cleared below
+            if (part && c * 128 + cplace[i & 1] >= g.K)
+                o = off[i] - (uint32_t)cplace[i & 1];
+            copy16_to_lds(i < 2 ? wbase : g.a, o, ring0 + stage * STAGE + i * 1024);
+        }
+    };
+    const int r = lane & 15, kq = lane >> 4;
+    v4i acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        acc[m] = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (wave + i * NW < chunks)
+            copy(wave + i * NW, i);
+    for (int c = wave, stage = 0; c < chunks; c += NW, stage = stage + 1 == R ? 0 : stage + 1) {
+        // the copies behind this chunk's stay in flight
+        if (c + (R - 1) * NW < chunks)
+            wait_copies<(R - 1) * COPIES>();
+        else
+            wait_copies<0>();
+        const char *st = ring + stage * STAGE;
+        v4i fw[2], fa[2][MT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            fw[s] = *reinterpret_cast<const v4i *>(st + r * 128 + place(r, s * 4 + kq) * 16);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int row = TC == 1 ? 16 + (r & 7) : 16 + m * 16 + r;
+                fa[s][m] = *reinterpret_cast<const v4i *>(st + row * 128 +
+                                                          place(row, s * 4 + kq) * 16);
+            }
+        }
+        if ((c + 1) * 128 > g.K) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (c * 128 + s * 64 + kq * 16 >= g.K)
+                    fw[s] = v4i{0, 0, 0, 0};
+        }
+        if (c + R * NW < chunks) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage has been read
+            copy(c + R * NW, stage);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s], fa[s][m], acc[m], 0, 0, 0);
+    }
+    __syncthreads();                                // every ring has been read
+    join_waves<MT, NW>(g, acc, reinterpret_cast<int *>(lds), n0, 0, out_dtype);
+}
+
+// ---------------------------------------------------------------------------
+// Operands that no 16-byte copy can address, any number of tokens: both go from
+// memory to the MFMA's registers directly, lane l holding 16 bytes of row
+// l % 16 at K offset 16 * (l / 16).  A workgroup owns 16 channels and MT * 16
+// tokens, its waves split K.  Channels are the MFMA's rows, so a lane ends up
+// with four consecutive channels of one token and stores them at once.
 // ---------------------------------------------------------------------------
 template <int MT, int NW>
 __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_dtype)
@@ -129,53 +281,12 @@ __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_
                     fw, load_tail(a[m] + k + s * 64, left), acc[m], 0, 0, 0);
         }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        *reinterpret_cast<v4i *>(&part[wave][m][lane * 4]) = acc[m];
-    __syncthreads();
-    for (int m = wave; m < MT; m += NW) {
-        v4i sum = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-            sum += *reinterpret_cast<const v4i *>(&part[i][m][lane * 4]);
-        const int v[4] = {sum[0], sum[1], sum[2], sum[3]};
-        const int t = t0 + m * 16 + r, n = n0 + (lane >> 4) * 4;
-        if (out_dtype == MOE_WNA16_BF16)
-            emit4<Bf16>(g, t, n, v);
-        else if (out_dtype == MOE_WNA16_FP16)
-            emit4<Fp16>(g, t, n, v);
-        else
-            emit4<float>(g, t, n, v);
-    }
+    join_waves<MT, NW>(g, acc, &part[0][0][0], n0, t0, out_dtype);
 }
 
 // ---------------------------------------------------------------------------
 // Many tokens: tiles through LDS.
 // ---------------------------------------------------------------------------
-
-// LDS byte address of a __shared__ pointer.
-__device__ __forceinline__ uint32_t lds_of(const void *p)
-{
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)(p);
-}
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// Lane l's 16 bytes at base + voff land at LDS address lds + l * 16.  base and
-// lds are wave-uniform.  Inline asm, so that the compiler does not make every
-// later LDS read wait for all copies in flight; the caller waits with vmcnt.
-__device__ __forceinline__ void copy16_to_lds(const int8_t *base_in, uint32_t voff, uint32_t lds_in)
-{
-    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_in);
-    const uint64_t b = reinterpret_cast<uintptr_t>(base_in);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
-    const void *base = reinterpret_cast<const void *>(((uint64_t)hi << 32) | (uint64_t)lo);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base),
-                 "s"(lds)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // Tile of BM tokens x BN channels, WM x WN waves, K in chunks of 128 bytes
 // (two MFMA steps).  Operand rows of 128 bytes sit in LDS as 8 pieces of 16
@@ -197,8 +308,6 @@ struct Tile8 {
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0, "copies divide evenly");
     // epilogue: each wave stages rows of its BN / WN channels
     static constexpr int WCOLS = BN / WN, REGION = 2 * STAGE / NW;
-
-    static __device__ __forceinline__ int place(int row, int c) { return c ^ ((row >> 1) & 7); }
 
     struct Frag {
         v4i a[MT], b[NT];
@@ -476,6 +585,13 @@ hipError_t launch_rows(const GemmArgs &g, int out_dtype, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <int TC, int NW, int R>
+hipError_t launch_stream(const GemmArgs &g, int out_dtype, hipStream_t stream)
+{
+    gemm_stream_kernel<TC, NW, R><<<(unsigned)((g.N + 15) / 16), 64 * NW, 0, stream>>>(g, out_dtype);
+    return hipGetLastError();
+}
+
 bool aligned16(const GemmArgs &g)
 {
     return (reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.w) |
@@ -509,11 +625,16 @@ hipError_t launch_gemm_w8a8(const GemmArgs &g, const GemmPlan &p, int out_dtype,
             return launch_tile<Tile8<256, 256, 2, 4>>(g, out_dtype, stream);
         return launch_tile<Tile8<128, 128, 2, 2>>(g, out_dtype, stream);
     }
-    if (g.T <= 16)
-        return launch_rows<1>(g, out_dtype, stream);
-    if (g.T <= 32)
-        return launch_rows<2>(g, out_dtype, stream);
-    return launch_rows<4>(g, out_dtype, stream);
+    if (p.variant == 0 && aligned16(g)) {
+        if (g.T <= 8)
+            return launch_stream<1, 16, 2>(g, out_dtype, stream);
+        if (g.T <= 16)
+            return launch_stream<2, 16, 2>(g, out_dtype, stream);
+        if (g.T <= 32)
+            return launch_stream<4, 8, 3>(g, out_dtype, stream);
+        return launch_stream<8, 8, 2>(g, out_dtype, stream);
+    }
+    return g.T <= 16 ? launch_rows<1>(g, out_dtype, stream) : launch_rows<4>(g, out_dtype, stream);
 }
 
 }  // namespace wna16
