@@ -293,21 +293,21 @@ __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_
 // bytes; piece c of row r is stored at place c ^ ((r >> 1) & 7), so that the
 // 16 rows that one operand read touches cover all banks once.
 //
-// Pipeline, two LDS stages and two sets of operand registers.  While the
+// Pipeline, ST LDS stages and two sets of operand registers.  While the
 // first step of chunk c is multiplied, the second step's operands are read;
 // then one barrier: every wave holds all it needs of chunk c, and chunk c + 1
-// has arrived; while the second step is multiplied, chunk c + 2 is copied over
+// has arrived; while the second step is multiplied, chunk c + ST is copied over
 // chunk c and the first operands of chunk c + 1 are read.
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Tile8 {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
-    static constexpr int KC = 128;
+    static constexpr int KC = 128, ST = ST_;
     static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
     static constexpr int STAGE = (BM + BN) * KC;
     static constexpr int ACOPIES = BM / 8 / NW, COPIES = (BM + BN) / 8 / NW;   // 8 rows each
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0, "copies divide evenly");
     // epilogue: each wave stages rows of its BN / WN channels
-    static constexpr int WCOLS = BN / WN, REGION = 2 * STAGE / NW;
+    static constexpr int WCOLS = BN / WN, REGION = ST * STAGE / NW;
 
     struct Frag {
         v4i a[MT], b[NT];
@@ -341,13 +341,18 @@ struct Tile8 {
                              lds + arow * KC + place(arow, 4 + kq) * 16};
         const char *bt[2] = {lds + brow * KC + place(brow, kq) * 16,
                              lds + brow * KC + place(brow, 4 + kq) * 16};
+        // operand i of MT + NT of a step
+        auto read_one = [&](Frag &f, int i, int stage, int s) {
+            if (i < NT)
+                f.b[i] = *reinterpret_cast<const v4i *>(bt[s] + stage * STAGE + i * 16 * KC);
+            else
+                f.a[i - NT] =
+                    *reinterpret_cast<const v4i *>(at[s] + stage * STAGE + (i - NT) * 16 * KC);
+        };
         auto read = [&](Frag &f, int stage, int s) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                f.b[n] = *reinterpret_cast<const v4i *>(bt[s] + stage * STAGE + n * 16 * KC);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                f.a[m] = *reinterpret_cast<const v4i *>(at[s] + stage * STAGE + m * 16 * KC);
+            for (int i = 0; i < MT + NT; ++i)
+                read_one(f, i, stage, s);
         };
         v4i acc[NT][MT];
 #pragma unroll
@@ -355,14 +360,27 @@ struct Tile8 {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 acc[n][m] = v4i{0, 0, 0, 0};
-        auto multiply = [&](const Frag &f) {
+        // A step's products, with `count` actions spread between them: a wave
+        // that issues its copies or reads in a row waits for the address unit
+        // (16 cycles a copy, shared by the workgroup's waves) with idle MFMAs.
+        auto multiply = [&](const Frag &f, auto count, auto &&act) {
+            constexpr int N = MT * NT, C = decltype(count)::value;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int j = 0; j < N; ++j) {
+                const int m = j / NT, n = j % NT;
+                acc[n][m] =
+                    __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[n], f.a[m], acc[n][m], 0, 0, 0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[n][m] =
-                        __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[n], f.a[m], acc[n][m], 0, 0, 0);
+                for (int i = j * C / N; i < (j + 1) * C / N; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    act(i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
         };
+        constexpr std::integral_constant<int, MT + NT> kReads{};
+        constexpr std::integral_constant<int, MT + NT + COPIES> kReadsAndCopies{};
+        constexpr std::integral_constant<int, 0> kNothing{};
         auto clear_past_k = [&](Frag &f, int k) {
             if (k + kq * 16 >= g.K) {
 #pragma unroll
@@ -373,7 +391,7 @@ struct Tile8 {
         const int chunks = (g.K + KC - 1) / KC;
         // The loop's copies are whole chunks; the last chunk may be a part.
         auto copy_whole = [&](int c) {
-            const uint32_t st = lds0 + (c & 1) * STAGE;
+            const uint32_t st = lds0 + c % ST * STAGE;
             const int8_t *a = abase + (long long)c * KC, *w = wbase + (long long)c * KC;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i)
@@ -386,7 +404,7 @@ struct Tile8 {
             }
             // K past the end (K is a multiple of 16): the row's first piece is
             // read again, and the channel operand's registers are cleared below
-            const uint32_t st = lds0 + (c & 1) * STAGE;
+            const uint32_t st = lds0 + c % ST * STAGE;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
                 const bool in = c * KC + cplace < g.K;
@@ -396,32 +414,49 @@ struct Tile8 {
             }
         };
         Frag f0, f1;
-        copy_any(0);
-        __builtin_amdgcn_s_waitcnt(0x0f70);                // vmcnt(0)
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+            if (i < chunks)
+                copy_any(i);
+        // chunk 0 has arrived; the ones behind it stay in flight
+        if (chunks >= ST)
+            wait_copies<(ST - 1) * COPIES>();
+        else
+            wait_copies<0>();
         __syncthreads();
-        if (chunks > 1)
-            copy_any(1);
         read(f0, 0, 0);
-        int c = 0;
-        for (; c + 2 < chunks; ++c) {
-            read(f1, c & 1, 1);
-            multiply(f0);
-            __builtin_amdgcn_s_waitcnt(0x0f70);            // chunk c + 1 has arrived
+        int c = 0, stage = 0;
+        for (; (c + ST + 1) * KC <= g.K; ++c) {
+            const int next = stage + 1 == ST ? 0 : stage + 1;
+            multiply(f0, kReads, [&](int i) { read_one(f1, i, stage, 1); });
+            wait_copies<(ST - 2) * COPIES>();              // chunk c + 1 has arrived
             __syncthreads();
-            copy_any(c + 2);
-            read(f0, (c + 1) & 1, 0);
-            multiply(f1);
+            const uint32_t st = lds0 + stage * STAGE;
+            const int8_t *a = abase + (long long)(c + ST) * KC;
+            const int8_t *w = wbase + (long long)(c + ST) * KC;
+            multiply(f1, kReadsAndCopies, [&](int i) {
+                if (i < MT + NT)
+                    read_one(f0, i, next, 0);
+                else
+                    copy16_to_lds(i - MT - NT < ACOPIES ? a : w, off[i - MT - NT],
+                                  st + (i - MT - NT) * NW * 1024);
+            });
+            stage = next;
         }
-        for (; c < chunks; ++c) {                          // the last two
-            read(f1, c & 1, 1);
+        for (; c < chunks; ++c) {                          // the last ones
+            const int next = stage + 1 == ST ? 0 : stage + 1;
+            read(f1, stage, 1);
             clear_past_k(f0, c * KC);
-            multiply(f0);
-            __builtin_amdgcn_s_waitcnt(0x0f70);
+            multiply(f0, kNothing, [](int) {});
+            wait_copies<0>();
             __syncthreads();
+            if (c + ST < chunks)
+                copy_any(c + ST);                          // part of a chunk
             if (c + 1 < chunks)
-                read(f0, (c + 1) & 1, 0);
+                read(f0, next, 0);
             clear_past_k(f1, c * KC + 64);
-            multiply(f1);
+            multiply(f1, kNothing, [](int) {});
+            stage = next;
         }
         epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, lds + wave * REGION);
     }
@@ -438,7 +473,8 @@ struct Tile8 {
     {
         constexpr int ROW = WCOLS * sizeof(T), PIECES = ROW / 16, EPP = 16 / sizeof(T);
         constexpr int MP = MT < 2 ? MT : 2;   // 16-row steps a pass
-        static_assert(MT % MP == 0 && PIECES >= 8 && MP * 16 * ROW <= REGION, "passes fit");
+        static_assert(MT % MP == 0 && PIECES >= 4 && MP * 16 * ROW <= REGION, "passes fit");
+        auto spread = [](int row) { return PIECES >= 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
         const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
         float sw[NT][4];
 #pragma unroll
@@ -469,7 +505,7 @@ struct Tile8 {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int byte = (n * 16 + kq * 4) * (int)sizeof(T);
-                    char *at = region + row * ROW + (((byte >> 4) ^ ((row >> 1) & 7)) << 4) +
+                    char *at = region + row * ROW + (((byte >> 4) ^ spread(row)) << 4) +
                                (byte & 15);
                     Out4<T> v;
 #pragma unroll
@@ -493,7 +529,7 @@ struct Tile8 {
                 const int id = i * 64 + lane, row = id / PIECES, c = id % PIECES;
                 const int t = t0 + p * MP * 16 + row, n = n0 + c * EPP;
                 const v4i v = *reinterpret_cast<const v4i *>(region + row * ROW +
-                                                             ((c ^ ((row >> 1) & 7)) << 4));
+                                                             ((c ^ spread(row)) << 4));
                 store_piece<T>(g, t, n, v);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -545,7 +581,7 @@ template <class C, class T>
 __global__ void __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[C::ST * C::STAGE];
     // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of
     // tiles, so its L2 serves neighbours that share an operand: tiles are
     // numbered down bands of kBand rows, so that the 32 an XCD runs at a time
@@ -600,19 +636,54 @@ bool aligned16(const GemmArgs &g)
 
 }  // namespace
 
+namespace {
+
+// The tiles, and what they cost in microseconds on an MI355X: launch, first
+// copies and epilogue once; a chunk of 128 K with one workgroup a CU, and with
+// two where their LDS allows it; every further tile of a CU.  Fitted to N and
+// T that fill the 256 CUs once, twice and four times, at K = 2048 and 4096.
+// Large tiles do a chunk's products in less time (2.5 POP/s, where the clock
+// falls for power; 64 x 64: 1.4), small ones cover few rows with more CUs.
+struct TileCost {
+    int bm, bn;
+    float once, chunk1, chunk2, more;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 10.6f, 1.73f, 0.f, 8.0f},   {128, 256, 9.0f, 0.80f, 0.f, 10.0f},
+    {128, 128, 8.3f, 0.41f, 0.f, 5.5f},    {128, 64, 5.3f, 0.324f, 0.542f, 1.3f},
+    {64, 64, 4.8f, 0.19f, 0.372f, 0.2f},
+};
+
+float tile_cost(const TileCost &c, int T, int N, int K)
+{
+    const long long tiles = (long long)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const float per_cu = (float)((tiles + 255) / 256), chunks = (float)((K + 127) / 128);
+    const float pairs = c.chunk2 > 0.f ? (float)((tiles + 255) / 256 / 2) : 0.f;
+    return c.once + chunks * (pairs * c.chunk2 + (per_cu - 2.f * pairs) * c.chunk1) +
+           (per_cu - 1.f) * c.more;
+}
+
+}  // namespace
+
 GemmPlan gemm_plan(int T, int N, int K)
 {
-    (void)K;
     GemmPlan p{};
     p.split = 1;
     if (T <= 64) {
         p.variant = 0;
-        p.bm = (T + 15) / 16 * 16;
+        p.bm = (T + 7) / 8 * 8;
         p.bn = 16;
-    } else {
-        p.variant = 1;
-        const long long big = (long long)((T + 255) / 256) * ((N + 255) / 256);
-        p.bm = p.bn = big >= 192 ? 256 : 128;
+        return p;
+    }
+    p.variant = 1;
+    float best = 0.f;
+    for (const TileCost &c : kTiles) {
+        const float t = tile_cost(c, T, N, K);
+        if (p.bm == 0 || t < best) {
+            best = t;
+            p.bm = c.bm;
+            p.bn = c.bn;
+        }
     }
     return p;
 }
@@ -622,17 +693,30 @@ hipError_t launch_gemm_w8a8(const GemmArgs &g, const GemmPlan &p, int out_dtype,
 {
     if (p.variant == 1 && aligned16(g)) {
         if (p.bm == 256)
-            return launch_tile<Tile8<256, 256, 2, 4>>(g, out_dtype, stream);
-        return launch_tile<Tile8<128, 128, 2, 2>>(g, out_dtype, stream);
+            return launch_tile<Tile8<256, 256, 2, 4, 2>>(g, out_dtype, stream);
+        if (p.bn == 256)
+            return launch_tile<Tile8<128, 256, 2, 4, 3>>(g, out_dtype, stream);
+        if (p.bn == 128)
+            return launch_tile<Tile8<128, 128, 2, 4, 4>>(g, out_dtype, stream);
+        if (p.bm == 128)
+            return launch_tile<Tile8<128, 64, 2, 2, 3>>(g, out_dtype, stream);
+        return launch_tile<Tile8<64, 64, 2, 2, 4>>(g, out_dtype, stream);
     }
     if (p.variant == 0 && aligned16(g)) {
+        // Up to 256 workgroups (one a CU): all of the LDS for one, so that most
+        // of its K is in flight at once (N = 4096, K = 4096, T = 4: 5.9 us, with
+        // half the waves 6.3 us).  More: two a CU, so that one starts while the
+        // other joins (N = 16384: 16.1 us against 18.5 us).
+        const bool one = g.N <= 16 * 256;
         if (g.T <= 8)
-            return launch_stream<1, 16, 2>(g, out_dtype, stream);
+            return one ? launch_stream<1, 16, 2>(g, out_dtype, stream)
+                       : launch_stream<1, 8, 3>(g, out_dtype, stream);
         if (g.T <= 16)
-            return launch_stream<2, 16, 2>(g, out_dtype, stream);
+            return one ? launch_stream<2, 16, 2>(g, out_dtype, stream)
+                       : launch_stream<2, 8, 2>(g, out_dtype, stream);
         if (g.T <= 32)
-            return launch_stream<4, 8, 3>(g, out_dtype, stream);
-        return launch_stream<8, 8, 2>(g, out_dtype, stream);
+            return launch_stream<4, 4, 3>(g, out_dtype, stream);
+        return launch_stream<8, 4, 2>(g, out_dtype, stream);
     }
     return g.T <= 16 ? launch_rows<1>(g, out_dtype, stream) : launch_rows<4>(g, out_dtype, stream);
 }
