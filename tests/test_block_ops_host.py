@@ -126,27 +126,26 @@ def test_product_workspace_is_checked():
 
 def test_conveniences_refuse_what_is_not_on_the_gpu():
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
-    for f in (lambda: M.add_rmsnorm(x, x[0]), lambda: M.route_topk(x, 2), lambda: M.swiglu_quant(x),
-              lambda: M.gemm_w8a8(x.to(torch.int8), x[:, 0].float(), x.to(torch.int8), x[:, 0].float())):
-        with pytest.raises(ValueError):
-            f()
-    with pytest.raises(TypeError):
-        M.add_rmsnorm([1.0], x[0])
-    with pytest.raises(ValueError):
+    i8, f = x.to(torch.int8), x[:, 0].float()
+    for call in (lambda: M.add_rmsnorm(x, x[0]), lambda: M.route_topk(x, 2), lambda: M.swiglu_quant(x),
+                 lambda: M.gemm_w8a8(i8, f, i8, f)):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
+    with pytest.raises(ValueError, match="2-D"):
         M.route_topk(x[0], 2)
 
 
-def test_shape_checks_of_the_conveniences():
-    from weight_only_bit_moe_amd import block_ops as B
-    dev = torch.device("cpu")
-    t = torch.zeros(4, 6)
-    assert B._rows(t, "t", (4, 6), torch.float32, dev) == 6
-    assert B._rows(t[:, 1:4], "t", (4, 3), torch.float32, dev) == 6
-    assert B._rows(t[:1].expand(1, 6), "t", (1, 6), torch.float32, dev) == 6
-    for bad, shape in ((t.t(), (6, 4)), (t[:1].expand(4, 6), (4, 6)), (t, (4, 5)), (t[:, ::2], (4, 3))):
-        with pytest.raises(ValueError):
-            B._rows(bad, "t", shape, torch.float32, dev)
+@pytest.mark.parametrize("call", [
+    lambda x: M.add_rmsnorm([1.0], x), lambda x: M.add_rmsnorm(None, x), lambda x: M.add_rmsnorm(x),
+    lambda x: M.add_rmsnorm(x, x, x, 1e-6), lambda x: M.add_rmsnorm(x, x, x=x),
+    lambda x: M.add_rmsnorm(x, x, epsilon=1e-6), lambda x: M.route_topk(x),
+    lambda x: M.route_topk(x, 2, None), lambda x: M.gemm_w8a8(x, x, x), lambda x: M.swiglu_quant(),
+    lambda x: M.swiglu_quant(x, 1.0), lambda x: M.gemm_w8a8(x, x, x, x, x)])
+def test_conveniences_refuse_other_arguments(call):
     with pytest.raises(TypeError):
-        B._rows(t, "t", (4, 6), torch.int8, dev)
-    with pytest.raises(ValueError):
-        B._flat(t[:, 1:4], "t", (4, 3), torch.float32, dev)
+        call(torch.zeros(2, 64))
+
+
+def test_conveniences_are_documented():
+    for f in (M.add_rmsnorm, M.route_topk, M.gemm_w8a8, M.swiglu_quant):
+        assert f.__doc__.startswith(f.__name__ + "(")

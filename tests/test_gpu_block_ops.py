@@ -393,7 +393,46 @@ def test_gemm_non_finite_scales_stay_in_their_row(dev):
         assert bool(torch.isfinite(out).all())
 
 
-# ---- empty calls, streams, graphs --------------------------------------------------
+# ---- refusals, empty calls, streams, graphs --------------------------------------------------
+
+def test_refusals_name_the_argument(dev):
+    x = torch.zeros(4, 64, dtype=BF, device=dev)
+    w, f = torch.ones(64, dtype=BF, device=dev), torch.ones(4, device=dev)
+    i8 = torch.zeros(4, 64, dtype=torch.int8, device=dev)
+    for call, kind, what in (
+            (lambda: M.add_rmsnorm(x, w.float()), TypeError, "weight"),
+            (lambda: M.add_rmsnorm(x, w[:32]), ValueError, "weight"),
+            (lambda: M.add_rmsnorm(x, w.cpu()), ValueError, "weight"),
+            (lambda: M.add_rmsnorm(x.double(), w.double()), TypeError, "x"),
+            (lambda: M.add_rmsnorm(x, w, x[:2]), ValueError, "residual"),
+            (lambda: M.add_rmsnorm(x.t(), w[:4]), ValueError, "x"),
+            (lambda: M.add_rmsnorm(x[:1].expand(4, 64), w), ValueError, "x"),
+            (lambda: M.add_rmsnorm(x, w, out=x[:, :32]), ValueError, "out"),
+            (lambda: M.add_rmsnorm(x, w, quant=True, q=x), TypeError, "q"),
+            (lambda: M.add_rmsnorm(x, w, quant=True, scale=f[:3]), ValueError, "scale"),
+            (lambda: M.add_rmsnorm(x, w, eps="a"), TypeError, ""),
+            (lambda: M.add_rmsnorm(x, w, eps=-1.0), M.MoeWna16Error, "moe_wna16_add_rmsnorm"),
+            (lambda: M.route_topk(x, 65), M.MoeWna16Error, "moe_wna16_route_topk"),
+            (lambda: M.route_topk(x, 0), ValueError, "topk"),
+            (lambda: M.route_topk(x, 2, score="tanh"), ValueError, "score"),
+            (lambda: M.route_topk(x, 2, score=3), TypeError, "score"),
+            (lambda: M.route_topk(x, 2, bias=w), TypeError, "bias"),
+            (lambda: M.route_topk(x, 2, groups=3), M.MoeWna16Error, "route_topk"),
+            (lambda: M.route_topk(x, 2, ids=torch.zeros(4, 2, device=dev)), TypeError, "ids"),
+            (lambda: M.gemm_w8a8(x, f, i8, f), TypeError, "a has"),
+            (lambda: M.gemm_w8a8(i8, f, i8[:, :32], f), ValueError, "w"),
+            (lambda: M.gemm_w8a8(i8, f[:2], i8, f), ValueError, "a_scale"),
+            (lambda: M.gemm_w8a8(i8, f, i8, f, addend=x[:, :4].float()), TypeError, "addend"),
+            (lambda: M.gemm_w8a8(i8, f, i8, f, out_dtype=torch.int8), TypeError, "out_dtype"),
+            (lambda: M.gemm_w8a8(i8, f, i8, f, out_dtype=2), TypeError, "out_dtype"),
+            (lambda: M.gemm_w8a8(i8, f, i8, f, out=x), ValueError, "out"),
+            (lambda: M.gemm_w8a8(i8, f, i8, f, workspace=f), TypeError, "workspace"),
+            (lambda: M.swiglu_quant(x[:, :63]), ValueError, "gu"),
+            (lambda: M.swiglu_quant(x, clamp=-1.0), M.MoeWna16Error, "swiglu_quant"),
+            (lambda: M.swiglu_quant(x, q=i8), ValueError, "q")):
+        with pytest.raises(kind, match=what):
+            call()
+
 
 def test_empty(dev):
     z = lambda *s, dtype=BF: torch.empty(*s, dtype=dtype, device=dev)  # noqa: E731

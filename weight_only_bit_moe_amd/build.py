@@ -1,4 +1,5 @@
-"""Build the gfx950 shared library libmoe_wna16.so in-tree with hipcc.
+"""Build the gfx950 shared library libmoe_wna16.so in-tree with hipcc, and the
+Python module _block_ops with g++.
 
     python -m weight_only_bit_moe_amd.build
 """
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_wna16.so")
+MODULE = os.path.join(PKG, "_block_ops.so")
 SOURCES = ["kernels.hip", "quantize.hip", "prepare.hip", "norm.hip", "route_topk.hip",
            "gemm_w8a8.hip", "api.hip", "block_api.hip"]
 ARCH = "gfx950"
@@ -57,7 +59,29 @@ def build(verbose: bool = False, jobs: int = 3) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_module(verbose)
     return LIB
+
+
+def build_module(verbose: bool = False) -> str:
+    """Compile the Python module _block_ops (host code) against torch's headers."""
+    import sysconfig
+
+    import torch
+    at = os.path.dirname(torch.__file__)
+    tmp = MODULE + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", "/opt/rocm/include", "-isystem", os.path.join(at, "include"),
+           "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "block_ops_module.cpp"), "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_hip"]
+    _run(cmd, verbose)
+    os.replace(tmp, MODULE)
+    return MODULE
 
 
 # Host-side sanitizer build: the C ABI's host code (api.hip, block_api.hip) and the oracle's C
