@@ -445,13 +445,16 @@ int moe_wna16_route_topk(const void *logits, const float *bias, int T, int E, in
  *   out     [T, N] of out_dtype, rows ldo apart; may be the addend itself
  *           (same rows), must not overlap the inputs otherwise
  *   workspace  moe_wna16_gemm_w8a8_workspace_size bytes, 256-byte aligned; NULL
- *           when that is 0.  All zero before its first use; every call leaves
- *           its counters zero.  Calls that overlap need one each.
+ *           when that is 0 (it is not when K is split: few output tiles, long
+ *           K).  Its first MOE_WNA16_GEMM_SYNC_BYTES bytes must be zero before
+ *           its first use; every call leaves them zero.  Calls that overlap
+ *           need one each.
  * T, N >= 0 (an empty output: no launch), 1 <= K <= 131071 (the sum of 131071
  * products of -128 * -128 is the last that fits int32), T and N up to 2^21, strides >=
  * the row's length and below 2^23.  Operands with 16-byte aligned rows (base
  * pointers, lda, ldw and K multiples of 16) take the fast path for T > 64.
  */
+#define MOE_WNA16_GEMM_SYNC_BYTES 4096
 int moe_wna16_gemm_w8a8_workspace_size(int T, int N, int K, size_t *bytes_out);
 int moe_wna16_gemm_w8a8(const int8_t *a, const float *a_scale, const int8_t *w,
                         const float *w_scale, const void *addend, int T, int N, int K,

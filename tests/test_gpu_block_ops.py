@@ -339,12 +339,53 @@ def test_gemm(dev, T, N, K, dt):
     assert torch.equal(acc, out)
 
 
-@pytest.mark.parametrize("T,N,K", [(4200, 2050, 512), (4096, 4096, 272), (6200, 2304, 144)])
+@pytest.mark.parametrize("T,N,K", [(4200, 2050, 512), (4096, 4096, 272), (6200, 2304, 144),
+                                   (2040, 2050, 4112), (4090, 4090, 1040), (1020, 4070, 2064),
+                                   (510, 4080, 2064), (250, 2000, 2064)])
 def test_gemm_large_tiles(dev, T, N, K):
     a, sa, w, sw, g = operands(T, N, K, "large")
     add = torch.randn(T, N, generator=g).to(BF)
     out = M.gemm_w8a8(a.to(dev), sa.to(dev), w.to(dev), sw.to(dev), addend=add.to(dev))
     check_gemm(a, sa, w, sw, add, out)
+
+
+@pytest.mark.parametrize("T,N,K", [(128, 512, 4112), (66, 150, 16400), (300, 130, 6160), (100, 64, 8208),
+                                   (70, 20, 131056)])
+def test_gemm_split_k(dev, T, N, K):
+    """Few output tiles and a long K: K is split, and the sums are joined in the workspace, whose
+    counters are back at zero after every call."""
+    assert M.moe_wna16_gemm_w8a8_workspace_size(T, N, K) > 0
+    ws = M.gemm_w8a8_workspace_for(T, N, K, dev)
+    ws[4096:] = 0x5A                                    # only the counters start at zero
+    for i in range(4):
+        a, sa, w, sw, g = operands(T, N, K, i)
+        add = torch.randn(T, N, generator=g).to(HF) if i % 2 else None
+        out = M.gemm_w8a8(a.to(dev), sa.to(dev), w.to(dev), sw.to(dev), out_dtype=HF, workspace=ws,
+                          addend=None if add is None else add.to(dev))
+        check_gemm(a, sa, w, sw, add, out)
+        assert not bool(ws[:4096].any())
+    assert torch.equal(out, M.gemm_w8a8(a.to(dev), sa.to(dev), w.to(dev), sw.to(dev), out_dtype=HF,
+                                        addend=add.to(dev)))     # a workspace of its own
+
+
+def test_gemm_split_k_graph_replays(dev):
+    T, N, K = 90, 130, 8192
+    a, sa, w, sw, g = operands(T, N, K, "graph")
+    d = [v.to(dev) for v in (a, sa, w, sw)]
+    for ws in (M.gemm_w8a8_workspace_for(T, N, K, dev), None):
+        M.gemm_w8a8(*d, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = M.gemm_w8a8(*d, workspace=ws)
+        for _ in range(4):
+            d[0].copy_(torch.randint(-127, 128, (T, K), generator=g, dtype=torch.int8))
+            want = M.gemm_w8a8(*d)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(want, held)
+            check_gemm(d[0].cpu(), sa, w, sw, None, held)
 
 
 def test_gemm_extreme_codes_fill_int32(dev):
@@ -410,7 +451,7 @@ def test_refusals_name_the_argument(dev):
             (lambda: M.add_rmsnorm(x, w, out=x[:, :32]), ValueError, "out"),
             (lambda: M.add_rmsnorm(x, w, quant=True, q=x), TypeError, "q"),
             (lambda: M.add_rmsnorm(x, w, quant=True, scale=f[:3]), ValueError, "scale"),
-            (lambda: M.add_rmsnorm(x, w, eps="a"), TypeError, ""),
+            (lambda: M.add_rmsnorm(x, w, eps="a"), TypeError, "number"),
             (lambda: M.add_rmsnorm(x, w, eps=-1.0), M.MoeWna16Error, "moe_wna16_add_rmsnorm"),
             (lambda: M.route_topk(x, 65), M.MoeWna16Error, "moe_wna16_route_topk"),
             (lambda: M.route_topk(x, 0), ValueError, "topk"),

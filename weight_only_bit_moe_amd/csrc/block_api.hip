@@ -12,6 +12,7 @@ namespace {
 constexpr long long kMaxStride = 1ll << 23;   // products: 256 rows stay within 32-bit offsets
 constexpr int kMaxGemmDim = 1 << 21;
 constexpr int kMaxGemmK = 131071;
+static_assert(wna16::kCounterBytes == MOE_WNA16_GEMM_SYNC_BYTES, "the header states it");
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -164,8 +165,12 @@ int moe_wna16_gemm_w8a8(const int8_t *a, const float *a_scale, const int8_t *w,
     g.N = N;
     g.K = K;
     g.out = out;
-    g.counters = static_cast<int32_t *>(workspace);
-    g.partial = nullptr;
+    g.split = plan.split;
+    if (plan.split > 1) {
+        g.counters = static_cast<int32_t *>(workspace);
+        g.partial = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) +
+                                                wna16::kCounterBytes);
+    }
     return hip_status(wna16::launch_gemm_w8a8(g, plan, out_dtype, stream));
 }
 

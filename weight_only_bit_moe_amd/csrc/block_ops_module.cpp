@@ -11,7 +11,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -19,6 +18,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 
@@ -159,6 +159,15 @@ int dtype_code(at::ScalarType t, const char *name)
 at::Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, c10::Device dev)
 {
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+}
+
+// A product's workspace: its counters zeroed, by a fill kernel (a captured call
+// replays it).
+at::Tensor fresh_workspace(int64_t bytes, c10::Device dev)
+{
+    at::Tensor t = empty({bytes}, at::kByte, dev);
+    t.narrow(0, 0, std::min<int64_t>(bytes, MOE_WNA16_GEMM_SYNC_BYTES)).zero_();
+    return t;
 }
 
 // The caller's tensor, or a new one.
@@ -398,7 +407,7 @@ PyObject *gemm_w8a8(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     } else {
         size_t bytes = 0;
         if (lib.gemm_w8a8_workspace_size((int)T, (int)N, (int)K, &bytes) == MOE_WNA16_OK && bytes)
-            ws = at::zeros({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+            ws = fresh_workspace((int64_t)bytes, dev);
     }
     launch("moe_wna16_gemm_w8a8", dev, [&](hipStream_t s) {
         return lib.gemm_w8a8((const int8_t *)a.data_ptr(), (const float *)sa,

@@ -313,8 +313,10 @@ struct Tile8 {
         v4i a[MT], b[NT];
     };
 
+    // The tile's sums over the chunks [c0, c1) of K, and whether to write them.
     template <class T>
-    static __device__ __forceinline__ void run(const GemmArgs &g, int t0, int n0, char *lds)
+    static __device__ __forceinline__ void run(const GemmArgs &g, int t0, int n0, int c0, int c1,
+                                               int tile, int slice, char *lds)
     {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -388,10 +390,10 @@ struct Tile8 {
                     f.b[n] = v4i{0, 0, 0, 0};
             }
         };
-        const int chunks = (g.K + KC - 1) / KC;
-        // The loop's copies are whole chunks; the last chunk may be a part.
+        // Chunk c to its stage.  The loop's copies are whole chunks; the last
+        // chunk of K may be a part.
         auto copy_whole = [&](int c) {
-            const uint32_t st = lds0 + c % ST * STAGE;
+            const uint32_t st = lds0 + (c - c0) % ST * STAGE;
             const int8_t *a = abase + (long long)c * KC, *w = wbase + (long long)c * KC;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i)
@@ -404,7 +406,7 @@ struct Tile8 {
             }
             // K past the end (K is a multiple of 16): the row's first piece is
             // read again, and the channel operand's registers are cleared below
-            const uint32_t st = lds0 + c % ST * STAGE;
+            const uint32_t st = lds0 + (c - c0) % ST * STAGE;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
                 const bool in = c * KC + cplace < g.K;
@@ -416,17 +418,18 @@ struct Tile8 {
         Frag f0, f1;
 #pragma unroll
         for (int i = 0; i < ST; ++i)
-            if (i < chunks)
-                copy_any(i);
-        // chunk 0 has arrived; the ones behind it stay in flight
-        if (chunks >= ST)
+            if (c0 + i < c1)
+                copy_any(c0 + i);
+        // the first chunk has arrived; the ones behind it stay in flight
+        if (c1 - c0 >= ST)
             wait_copies<(ST - 1) * COPIES>();
         else
             wait_copies<0>();
         __syncthreads();
         read(f0, 0, 0);
-        int c = 0, stage = 0;
-        for (; (c + ST + 1) * KC <= g.K; ++c) {
+        int c = c0, stage = 0;
+        const int whole = c1 * KC <= g.K ? c1 : c1 - 1;
+        for (; c + ST < whole; ++c) {
             const int next = stage + 1 == ST ? 0 : stage + 1;
             multiply(f0, kReads, [&](int i) { read_one(f1, i, stage, 1); });
             wait_copies<(ST - 2) * COPIES>();              // chunk c + 1 has arrived
@@ -443,22 +446,78 @@ struct Tile8 {
             });
             stage = next;
         }
-        for (; c < chunks; ++c) {                          // the last ones
+        for (; c < c1; ++c) {                              // the last ones
             const int next = stage + 1 == ST ? 0 : stage + 1;
             read(f1, stage, 1);
             clear_past_k(f0, c * KC);
             multiply(f0, kNothing, [](int) {});
             wait_copies<0>();
             __syncthreads();
-            if (c + ST < chunks)
+            if (c + ST < c1)
                 copy_any(c + ST);                          // part of a chunk
-            if (c + 1 < chunks)
+            if (c + 1 < c1)
                 read(f0, next, 0);
             clear_past_k(f1, c * KC + 64);
             multiply(f1, kNothing, [](int) {});
             stage = next;
         }
-        epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, lds + wave * REGION);
+        if (g.split == 1 || join(g, acc, tile, slice))
+            epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, lds + wave * REGION);
+    }
+
+    // Split K: every workgroup of a tile leaves its int32 sums in the workspace
+    // and counts itself; the last one adds the others' to its own and writes the
+    // tile (true), so nobody waits, and since the sums are integers the order
+    // changes nothing.  The sums are written past the XCDs' caches (agent
+    // scope), and counted only when every wave's have arrived.
+    static __device__ __forceinline__ bool join(const GemmArgs &g, v4i (&acc)[NT][MT], int tile,
+                                                int slice)
+    {
+        __shared__ int s_count;
+        constexpr int PER = NT * MT * 2 * 64 * NW;         // 8-byte words of a tile's sums
+        uint64_t *sums = reinterpret_cast<uint64_t *>(g.partial) + (size_t)tile * g.split * PER;
+        const int at = (int)(threadIdx.x >> 6) * (NT * MT * 2 * 64) + (int)(threadIdx.x & 63);
+        uint64_t *own = sums + (size_t)slice * PER + at;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t v = (uint32_t)acc[n][m][2 * h] |
+                                       (uint64_t)(uint32_t)acc[n][m][2 * h + 1] << 32;
+                    __hip_atomic_store(own + ((n * MT + m) * 2 + h) * 64, v, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+                }
+        wait_copies<0>();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int32_t *count = g.counters + tile;
+            s_count = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (s_count == g.split - 1)
+                __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (s_count != g.split - 1)
+            return false;
+        for (int i = 0; i < g.split; ++i) {
+            if (i == slice)
+                continue;
+            const uint64_t *other = sums + (size_t)i * PER + at;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t v =
+                            __hip_atomic_load(other + ((n * MT + m) * 2 + h) * 64, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+                        acc[n][m][2 * h] += (int)(uint32_t)v;
+                        acc[n][m][2 * h + 1] += (int)(uint32_t)(v >> 32);
+                    }
+        }
+        return true;
     }
 
     // A lane holds four consecutive channels of one token per 16 x 16 result:
@@ -586,21 +645,25 @@ gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
     // tiles, so its L2 serves neighbours that share an operand: tiles are
     // numbered down bands of kBand rows, so that the 32 an XCD runs at a time
     // are about as many rows as columns.
-    const int total = tiles_m * tiles_n, per = (total + 7) / 8;
-    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int total = tiles_m * tiles_n * g.split, per = (total + 7) / 8;
+    int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (id >= total || (int)(blockIdx.x >> 3) >= per)
         return;
+    const int slice = id % g.split;
+    id /= g.split;
     const int band = id / (kBand * tiles_n), rest = id - band * (kBand * tiles_n);
     const int rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
     const int tm = band * kBand + rest % rows, tn = rest / rows;
-    C::template run<T>(g, tm * C::BM, tn * C::BN, lds);
+    const int chunks = (g.K + C::KC - 1) / C::KC;
+    C::template run<T>(g, tm * C::BM, tn * C::BN, slice * chunks / g.split,
+                       (slice + 1) * chunks / g.split, id, slice, lds);
 }
 
 template <class C>
 hipError_t launch_tile(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     const int tm = (g.T + C::BM - 1) / C::BM, tn = (g.N + C::BN - 1) / C::BN;
-    const unsigned grid = (unsigned)((tm * tn + 7) / 8 * 8);
+    const unsigned grid = (unsigned)((tm * tn * g.split + 7) / 8 * 8);
     auto go = [&](auto kernel) {
         kernel<<<grid, 64 * C::NW, 0, stream>>>(g, tm, tn);
         return hipGetLastError();
@@ -639,28 +702,37 @@ bool aligned16(const GemmArgs &g)
 namespace {
 
 // The tiles, and what they cost in microseconds on an MI355X: launch, first
-// copies and epilogue once; a chunk of 128 K with one workgroup a CU, and with
-// two where their LDS allows it; every further tile of a CU.  Fitted to N and
-// T that fill the 256 CUs once, twice and four times, at K = 2048 and 4096.
+// copies and epilogue once; a chunk of 128 K with one workgroup a CU, when few
+// CUs run one and when all do; a chunk for each of two workgroups a CU, where
+// their LDS allows it; every further tile of a CU.  Fitted to N and T that fill
+// the 256 CUs in part, once, twice and four times, at K from 2048 to 16384.
 // Large tiles do a chunk's products in less time (2.5 POP/s, where the clock
 // falls for power; 64 x 64: 1.4), small ones cover few rows with more CUs.
 struct TileCost {
     int bm, bn;
-    float once, chunk1, chunk2, more;
+    float once, few, all, two, more;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 10.6f, 1.73f, 0.f, 8.0f},   {128, 256, 9.0f, 0.80f, 0.f, 10.0f},
-    {128, 128, 8.3f, 0.41f, 0.f, 5.5f},    {128, 64, 5.3f, 0.324f, 0.542f, 1.3f},
-    {64, 64, 4.8f, 0.19f, 0.372f, 0.2f},
+    {256, 256, 10.6f, 1.30f, 1.73f, 0.f, 8.0f}, {128, 256, 9.5f, 0.50f, 0.80f, 0.f, 10.0f},
+    {128, 128, 7.3f, 0.326f, 0.43f, 0.f, 5.5f}, {128, 64, 5.5f, 0.255f, 0.30f, 0.542f, 1.3f},
+    {64, 64, 4.8f, 0.163f, 0.19f, 0.372f, 0.2f},
 };
+constexpr int kMaxSplit = 16;
 
-float tile_cost(const TileCost &c, int T, int N, int K)
+// With K split over `split` workgroups a tile, the chunks are fewer, every
+// workgroup writes its sums and the last one of a tile reads the others'.
+// N = 512, T = 128, K = 16384 (64 x 64 tiles): 25.7 us whole, 12.4 us in eight;
+// K = 4096: 10.1 us whole, 9.0 us in four, 10.6 us in eight.
+float tile_cost(const TileCost &c, long long tiles, int chunks, int split)
 {
-    const long long tiles = (long long)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    const float per_cu = (float)((tiles + 255) / 256), chunks = (float)((K + 127) / 128);
-    const float pairs = c.chunk2 > 0.f ? (float)((tiles + 255) / 256 / 2) : 0.f;
-    return c.once + chunks * (pairs * c.chunk2 + (per_cu - 2.f * pairs) * c.chunk1) +
-           (per_cu - 1.f) * c.more;
+    const long long groups = tiles * split;
+    const float per_cu = (float)((groups + 255) / 256), each = (float)((chunks + split - 1) / split);
+    const float pairs = c.two > 0.f ? (float)((groups + 255) / 256 / 2) : 0.f;
+    const float one = c.few + (c.all - c.few) * (groups < 256 ? (float)groups / 256.f : 1.f);
+    const float join =
+        split > 1 ? 1.f + 0.35f * split + 0.006f / 4096.f * c.bm * c.bn * (float)groups : 0.f;
+    return c.once + each * (pairs * c.two + (per_cu - 2.f * pairs) * one) + (per_cu - 1.f) * c.more +
+           join;
 }
 
 }  // namespace
@@ -677,14 +749,22 @@ GemmPlan gemm_plan(int T, int N, int K)
     }
     p.variant = 1;
     float best = 0.f;
-    for (const TileCost &c : kTiles) {
-        const float t = tile_cost(c, T, N, K);
-        if (p.bm == 0 || t < best) {
-            best = t;
-            p.bm = c.bm;
-            p.bn = c.bn;
+    for (const TileCost &c : kTiles)
+        for (int split = 1; split <= kMaxSplit; split *= 2) {
+            const long long tiles = (long long)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+            // at least two chunks a slice; the GPU is not filled twice to split
+            if (split > 1 && (tiles * split > 512 || (K + 127) / 128 < 2 * split))
+                break;
+            const float t = tile_cost(c, tiles, (K + 127) / 128, split);
+            if (p.bm == 0 || t < best) {
+                best = t;
+                p.bm = c.bm;
+                p.bn = c.bn;
+                p.split = split;
+                p.workspace = split == 1 ? 0
+                                         : kCounterBytes + (size_t)tiles * split * c.bm * c.bn * 4;
+            }
         }
-    }
     return p;
 }
 

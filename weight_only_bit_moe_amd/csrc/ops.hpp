@@ -54,14 +54,18 @@ struct GemmArgs {
     long long lda, ldw, ld_add, ldo;            // elements between rows
     int T, N, K;
     void *out;
-    int32_t *counters;                          // zero between calls (split K)
-    int32_t *partial;                           // int32 partial sums (split K)
+    int split;                                  // K slices a tile, each its own workgroup
+    int32_t *counters;                          // [tiles], zero between calls (split > 1)
+    int32_t *partial;                           // [tiles][split] int32 sums (split > 1)
 };
+// Start of a product's workspace: the counters, at most one for each of the 512
+// workgroups of a split product, then the partial sums.
+constexpr size_t kCounterBytes = 4096;          // MOE_WNA16_GEMM_SYNC_BYTES
 // Tiling of a product: a pure function of the sizes.
 struct GemmPlan {
-    int variant;                                // 0: rows in registers (few tokens), 1: LDS tiles
+    int variant;                                // 0: few tokens, weights streamed, 1: tiles
     int bm, bn;                                 // output tile
-    int split;                                  // K slices, each its own workgroup
+    int split;                                  // K slices a tile
     size_t workspace;                           // bytes
 };
 GemmPlan gemm_plan(int T, int N, int K);
