@@ -1,0 +1,149 @@
+"""One mixture-of-experts block of a decoder, as a serving step runs it:
+
+    h, y, q = residual addition, root-mean-square norm, y in 8 bits   add_rmsnorm
+    logits  = y @ gate.T                                              torch
+    ids, w  = expert routing                                          route_topk
+    out     = routed experts of y                                     forward
+    out    += shared expert of q: product, SwiGLU in 8 bits, product  gemm_w8a8, swiglu_quant
+
+and returns out and h, the residual stream that the next norm adds out to.
+
+    python -m weight_only_bit_moe_amd.block --tokens 4      # time of a step on synthetic weights
+"""
+from __future__ import annotations
+
+import dataclasses
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding, block_ops
+
+
+def channel_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of a weight in 8 bits: codes int8 and a float32 scale for each row (channel), the
+    largest magnitude of a row at 127.  Done once, when weights are loaded."""
+    top = w.float().abs().amax(-1)
+    inv = torch.where(top > 0, 127.0 / top, torch.zeros_like(top))
+    return torch.round(w.float() * inv[:, None]).to(torch.int8), top / 127.0
+
+
+@dataclasses.dataclass
+class MoEBlock:
+    """Weights and routing of one block.  The routed experts' tensors are forward()'s; the shared
+    expert's are int8 codes with a scale for each channel (channel_codes).  Workspaces are made
+    for a token count on its first use and kept; a block runs one step at a time."""
+
+    norm: torch.Tensor                      # [H] bf16
+    gate: torch.Tensor                      # [E, H] bf16, router
+    w13: torch.Tensor                       # routed experts: codes and scales
+    s13: torch.Tensor
+    w2: torch.Tensor
+    s2: torch.Tensor
+    bits: Tuple[int, int]
+    group: Tuple[int, int]
+    shared13: torch.Tensor                  # [2 Is, H] int8, gate rows then up rows
+    shared13_scale: torch.Tensor            # [2 Is] float32
+    shared2: torch.Tensor                   # [H, Is] int8
+    shared2_scale: torch.Tensor             # [H] float32
+    topk: int
+    bias: Optional[torch.Tensor] = None     # [E] float32, balance
+    score: str = "softmax"
+    groups: int = 1
+    topk_groups: int = 1
+    renormalize: bool = True
+    route_scale: float = 1.0
+    alpha: float = 1.0
+    beta: float = 0.0
+    clamp: Optional[float] = None
+    eps: float = 1e-6
+    _kept: dict = dataclasses.field(default_factory=dict, repr=False)
+
+    def _workspaces(self, T: int, device):
+        ws = self._kept.get(T)
+        if ws is None:
+            H, E, I = self.norm.numel(), self.w13.shape[0], self.w13.shape[1] // 2
+            two_is, Is = self.shared13.shape[0], self.shared2.shape[1]
+            ws = (binding.workspace_for(T, H, I, E, self.topk, device),
+                  block_ops.gemm_w8a8_workspace_for(T, two_is, H, device),
+                  block_ops.gemm_w8a8_workspace_for(T, H, Is, device))
+            self._kept[T] = ws
+        return ws
+
+    def route(self, y: torch.Tensor):
+        """Expert ids and routing weights of normed rows y [T, H] bf16."""
+        logits = torch.nn.functional.linear(y, self.gate)
+        return block_ops.route_topk(logits, self.topk, bias=self.bias, score=self.score,
+                                    groups=self.groups, topk_groups=self.topk_groups,
+                                    renormalize=self.renormalize, scale=self.route_scale)
+
+    def shared(self, q, scale, addend, workspaces=(None, None)):
+        """The shared expert of rows in 8 bits, added to `addend` [T, H] bf16 in place."""
+        gu = block_ops.gemm_w8a8(q, scale, self.shared13, self.shared13_scale,
+                                 workspace=workspaces[0])
+        aq, ascale = block_ops.swiglu_quant(gu, alpha=self.alpha, beta=self.beta, clamp=self.clamp)
+        return block_ops.gemm_w8a8(aq, ascale, self.shared2, self.shared2_scale, addend=addend,
+                                   out=addend, workspace=workspaces[1])
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
+        """x [T, H] bf16, the block's input, and the residual stream it is added to (None at the
+        start of the stack).  Returns (out, residual stream)."""
+        layer_ws, ws13, ws2 = self._workspaces(x.shape[0], x.device)
+        n = block_ops.add_rmsnorm(x, self.norm, residual, eps=self.eps, quant=True)
+        ids, w = self.route(n["y"])
+        out = binding.forward(n["y"], ids, w, self.w13, self.s13, self.w2, self.s2, bits=self.bits,
+                              group=self.group, alpha=self.alpha, beta=self.beta, clamp=self.clamp,
+                              workspace=layer_ws)
+        return self.shared(n["q"], n["scale"], out, (ws13, ws2)), n.get("residual", x)
+
+
+def synthetic(spec, seed: int, device, shared: int = 0) -> MoEBlock:
+    """A block with the random routed experts of an inputs.LayerSpec (its T and routing are not
+    used) and random other weights; shared: the shared expert's intermediate size (0: spec.I)."""
+    import numpy as np
+
+    from .inputs import make_layer
+    L = make_layer(dataclasses.replace(spec, T=1), seed)
+    Is = shared or spec.I
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    randn = lambda *s: torch.randn(*s, generator=g, device=device)  # noqa: E731
+    c13, sc13 = channel_codes(randn(2 * Is, spec.H) * spec.H ** -0.5)
+    c2, sc2 = channel_codes(randn(spec.H, Is) * Is ** -0.5)
+    dev = lambda a: torch.from_numpy(a).to(device)  # noqa: E731
+    return MoEBlock(
+        norm=(1 + 0.1 * randn(spec.H)).bfloat16(), gate=(randn(spec.E, spec.H) * spec.H ** -0.5).bfloat16(),
+        w13=dev(L.w13.view(np.int32)), s13=dev(L.s13), w2=dev(L.w2.view(np.int32)), s2=dev(L.s2),
+        bits=(spec.bits13, spec.bits2), group=(spec.group13, spec.group2), shared13=c13,
+        shared13_scale=sc13, shared2=c2, shared2_scale=sc2, topk=spec.topk, bias=0.05 * randn(spec.E),
+        score="sigmoid", route_scale=1.0, alpha=spec.alpha, beta=spec.beta,
+        clamp=None if math.isinf(spec.clamp) else spec.clamp)
+
+
+def main() -> None:
+    import argparse
+    import time
+
+    from .inputs import CONFIGS
+    ap = argparse.ArgumentParser(description="Time of one block's step on synthetic weights "
+                                             "(hidden 4096, 256 experts of 2048, 2-bit codes).")
+    ap.add_argument("--tokens", type=int, default=4)
+    ap.add_argument("--steps", type=int, default=100)
+    a = ap.parse_args()
+    dev = torch.device("cuda:0")
+    block = synthetic(CONFIGS[2], 1, dev)
+    H = CONFIGS[2].H
+    x, r = (torch.randn(a.tokens, H, device=dev).bfloat16() for _ in range(2))
+    for _ in range(5):
+        out, h = block(x, r)
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(a.steps):
+        out, h = block(x, r)
+    torch.cuda.synchronize()
+    print(f"{a.tokens} tokens: {(time.perf_counter() - t) / a.steps * 1e6:.1f} us a step")
+
+
+if __name__ == "__main__":
+    main()
