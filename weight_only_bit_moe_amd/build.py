@@ -77,8 +77,8 @@ def build_module(verbose: bool = False) -> str:
            "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "block_ops_module.cpp"), "-o", tmp,
-           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-           "-lc10_hip"]
+           "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_hip", "-lc10", "-lc10_hip"]
     _run(cmd, verbose)
     os.replace(tmp, MODULE)
     return MODULE

@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -158,7 +158,7 @@ int dtype_code(at::ScalarType t, const char *name)
 
 at::Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, c10::Device dev)
 {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+    return at::detail::empty_cuda(shape, dtype, dev, std::nullopt);   // at::empty, undispatched
 }
 
 // A product's workspace: its counters zeroed, by a fill kernel (a captured call
