@@ -18,38 +18,57 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 
 template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Out4 { T v[4]; };
 
-// Four consecutive outputs of one token, from column n.
+// What four consecutive outputs of one token, from column n, need besides
+// their sums: loaded while the operands are on their way.
 template <class T>
-__device__ __forceinline__ void emit4(const GemmArgs &g, int t, int n, const int (&acc)[4])
-{
-    if (t >= g.T || n >= g.N)
-        return;
-    const float sa = g.a_scale[t];
-    const T *add = g.addend ? static_cast<const T *>(g.addend) + t * g.ld_add + n : nullptr;
-    T *o = static_cast<T *>(g.out) + t * g.ldo + n;
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = n + i < g.N ? (float)acc[i] * sa * g.w_scale[n + i] : 0.f;
-    if (n + 4 <= g.N) {
-        if (add) {
-            const Out4<T> d = *reinterpret_cast<const Out4<T> *>(add);
+struct Beside {
+    float sa, sw[4];
+    Out4<T> add;
+
+    __device__ __forceinline__ void load(const GemmArgs &g, int t, int n)
+    {
+        add = Out4<T>{};
+        if (t >= g.T || n >= g.N)
+            return;
+        sa = g.a_scale[t];
+        const T *p = static_cast<const T *>(g.addend) + t * g.ld_add + n;
+        if (n + 4 <= g.N) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                f[i] += to_float(d.v[i]);
+                sw[i] = g.w_scale[n + i];
+            if (g.addend)
+                add = *reinterpret_cast<const Out4<T> *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < g.N) {
+                    sw[i] = g.w_scale[n + i];
+                    if (g.addend)
+                        add.v[i] = p[i];
+                }
         }
+    }
+    __device__ __forceinline__ void emit(const GemmArgs &g, int t, int n, v4i acc) const
+    {
+        if (t >= g.T || n >= g.N)
+            return;
+        T *o = static_cast<T *>(g.out) + t * g.ldo + n;
         Out4<T> r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r.v[i] = from_float<T>(f[i]);
-        *reinterpret_cast<Out4<T> *>(o) = r;
-    } else {
+        for (int i = 0; i < 4; ++i) {
+            const float f = (float)acc[i] * sa * sw[i];
+            r.v[i] = from_float<T>(g.addend ? f + to_float(add.v[i]) : f);
+        }
+        if (n + 4 <= g.N) {
+            *reinterpret_cast<Out4<T> *>(o) = r;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < g.N)
-                o[i] = from_float<T>(add ? f[i] + to_float(add[i]) : f[i]);
+            for (int i = 0; i < 4; ++i)
+                if (n + i < g.N)
+                    o[i] = r.v[i];
+        }
     }
-}
+};
 
 // 16 bytes from any address; gfx950 loads them unaligned.
 struct __attribute__((packed, aligned(1))) Bytes16 { int v[4]; };
@@ -105,29 +124,24 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Sums the waves' 16-channel x MT*16-token results and writes them.
-template <int MT, int NW>
+// Sums the waves' 16-channel x MT*16-token results; wave m writes tokens
+// [t0 + 16m, +16), for which it holds `beside`.
+template <class T, int MT, int NW>
 __device__ __forceinline__ void join_waves(const GemmArgs &g, const v4i (&acc)[MT], int *part,
-                                           int n0, int t0, int out_dtype)
+                                           int n0, int t0, const Beside<T> &beside)
 {
+    static_assert(MT <= NW, "a wave for every 16 tokens");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
         *reinterpret_cast<v4i *>(part + ((wave * MT + m) * 64 + lane) * 4) = acc[m];
     __syncthreads();
-    for (int m = wave; m < MT; m += NW) {
+    if (wave < MT) {
         v4i sum = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < NW; ++i)
-            sum += *reinterpret_cast<const v4i *>(part + ((i * MT + m) * 64 + lane) * 4);
-        const int v[4] = {sum[0], sum[1], sum[2], sum[3]};
-        const int t = t0 + m * 16 + (lane & 15), n = n0 + (lane >> 4) * 4;
-        if (out_dtype == MOE_WNA16_BF16)
-            emit4<Bf16>(g, t, n, v);
-        else if (out_dtype == MOE_WNA16_FP16)
-            emit4<Fp16>(g, t, n, v);
-        else
-            emit4<float>(g, t, n, v);
+            sum += *reinterpret_cast<const v4i *>(part + ((i * MT + wave) * 64 + lane) * 4);
+        beside.emit(g, t0 + wave * 16 + (lane & 15), n0 + (lane >> 4) * 4, sum);
     }
 }
 
@@ -141,8 +155,8 @@ __device__ __forceinline__ void join_waves(const GemmArgs &g, const v4i (&acc)[M
 // address unit takes one lane a cycle; the copies take eight lanes of one row
 // in a row, four lanes a cycle.
 // ---------------------------------------------------------------------------
-template <int TC, int NW, int R>
-__global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g, int out_dtype)
+template <class T, int TC, int NW, int R>
+__global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g)
 {
     constexpr int MT = TC < 2 ? 1 : TC / 2, ROWS = 16 + 8 * TC, STAGE = ROWS * 128;
     constexpr int COPIES = ROWS / 8, RING = NW * R * STAGE, PART = NW * MT * 1024;
@@ -179,6 +193,9 @@ __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g, int ou
         }
     };
     const int r = lane & 15, kq = lane >> 4;
+    Beside<T> beside;
+    if (wave < MT)
+        beside.load(g, wave * 16 + r, n0 + kq * 4);
     v4i acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g, int ou
                 acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s], fa[s][m], acc[m], 0, 0, 0);
     }
     __syncthreads();                                // every ring has been read
-    join_waves<MT, NW>(g, acc, reinterpret_cast<int *>(lds), n0, 0, out_dtype);
+    join_waves<T, MT, NW>(g, acc, reinterpret_cast<int *>(lds), n0, 0, beside);
 }
 
 // ---------------------------------------------------------------------------
@@ -232,13 +249,16 @@ __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g, int ou
 // tokens, its waves split K.  Channels are the MFMA's rows, so a lane ends up
 // with four consecutive channels of one token and stores them at once.
 // ---------------------------------------------------------------------------
-template <int MT, int NW>
-__global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_dtype)
+template <class T, int MT, int NW>
+__global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g)
 {
     __shared__ int part[NW][MT][256];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (MT * 16);
     const int r = lane & 15, kc = (lane >> 4) * 16;
+    Beside<T> beside;
+    if (wave < MT)
+        beside.load(g, t0 + wave * 16 + r, n0 + (lane >> 4) * 4);
     const int nr = n0 + r < g.N ? n0 + r : g.N - 1;     // rows past the end repeat the last
     const int8_t *w = g.w + nr * g.ldw + kc;
     const int8_t *a[MT];
@@ -281,7 +301,7 @@ __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g, int out_
                     fw, load_tail(a[m] + k + s * 64, left), acc[m], 0, 0, 0);
         }
     }
-    join_waves<MT, NW>(g, acc, &part[0][0][0], n0, t0, out_dtype);
+    join_waves<T, MT, NW>(g, acc, &part[0][0][0], n0, t0, beside);
 }
 
 // ---------------------------------------------------------------------------
@@ -311,6 +331,24 @@ struct Tile8 {
 
     struct Frag {
         v4i a[MT], b[NT];
+    };
+    // of the lane's tokens t + 16m and channels n + 16j .. + 3; past the end the last one's
+    struct Scales {
+        float sa[MT], sw[NT][4];
+
+        __device__ __forceinline__ void load(const GemmArgs &g, int t, int n)
+        {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = n + j * 16 + i;
+                    sw[j][i] = g.w_scale[col < g.N ? col : g.N - 1];
+                }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                sa[m] = g.a_scale[t + m * 16 < g.T ? t + m * 16 : g.T - 1];
+        }
     };
 
     // The tile's sums over the chunks [c0, c1) of K, and whether to write them.
@@ -446,6 +484,12 @@ struct Tile8 {
             });
             stage = next;
         }
+        // The scales are on their way while the last chunks are multiplied, where
+        // registers are left for them.
+        constexpr bool kEarly = NT * MT < 32;
+        Scales sc;
+        if (kEarly)
+            sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
         for (; c < c1; ++c) {                              // the last ones
             const int next = stage + 1 == ST ? 0 : stage + 1;
             read(f1, stage, 1);
@@ -461,8 +505,10 @@ struct Tile8 {
             multiply(f1, kNothing, [](int) {});
             stage = next;
         }
+        if (!kEarly)
+            sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
         if (g.split == 1 || join(g, acc, tile, slice))
-            epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, lds + wave * REGION);
+            epilogue<T>(g, t0 + wm * (MT * 16), n0 + wn * WCOLS, acc, sc, lds + wave * REGION);
     }
 
     // Split K: every workgroup of a tile leaves its int32 sums in the workspace
@@ -528,25 +574,14 @@ struct Tile8 {
     // operands are.
     template <class T>
     static __device__ __forceinline__ void epilogue(const GemmArgs &g, int t0, int n0,
-                                                    const v4i (&acc)[NT][MT], char *region)
+                                                    const v4i (&acc)[NT][MT], const Scales &sc,
+                                                    char *region)
     {
         constexpr int ROW = WCOLS * sizeof(T), PIECES = ROW / 16, EPP = 16 / sizeof(T);
         constexpr int MP = MT < 2 ? MT : 2;   // 16-row steps a pass
         static_assert(MT % MP == 0 && PIECES >= 4 && MP * 16 * ROW <= REGION, "passes fit");
         auto spread = [](int row) { return PIECES >= 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
         const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
-        float sw[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = n0 + n * 16 + kq * 4 + i;
-                sw[n][i] = g.w_scale[col < g.N ? col : g.N - 1];
-            }
-        float sa[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            sa[m] = g.a_scale[t0 + m * 16 + r < g.T ? t0 + m * 16 + r : g.T - 1];
 #pragma unroll
         for (int p = 0; p < MT / MP; ++p) {
             Out4<T> add[MP][NT];
@@ -569,7 +604,7 @@ struct Tile8 {
                     Out4<T> v;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float f = (float)acc[n][m][i] * sa[m] * sw[n][i];
+                        float f = (float)acc[n][m][i] * sc.sa[m] * sc.sw[n][i];
                         if (g.addend)
                             f += to_float(add[mm][n].v[i]);
                         v.v[i] = from_float<T>(f);
@@ -659,20 +694,27 @@ gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
                        (slice + 1) * chunks / g.split, id, slice, lds);
 }
 
+// f(a value of the output type), then the launch's status.
+template <class F>
+hipError_t with_type(int out_dtype, F &&f)
+{
+    if (out_dtype == MOE_WNA16_BF16)
+        f(Bf16{});
+    else if (out_dtype == MOE_WNA16_FP16)
+        f(Fp16{});
+    else
+        f(0.f);
+    return hipGetLastError();
+}
+
 template <class C>
 hipError_t launch_tile(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     const int tm = (g.T + C::BM - 1) / C::BM, tn = (g.N + C::BN - 1) / C::BN;
     const unsigned grid = (unsigned)((tm * tn * g.split + 7) / 8 * 8);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, 64 * C::NW, 0, stream>>>(g, tm, tn);
-        return hipGetLastError();
-    };
-    if (out_dtype == MOE_WNA16_BF16)
-        return go(gemm_tile_kernel<C, Bf16>);
-    if (out_dtype == MOE_WNA16_FP16)
-        return go(gemm_tile_kernel<C, Fp16>);
-    return go(gemm_tile_kernel<C, float>);
+    return with_type(out_dtype, [&](auto zero) {
+        gemm_tile_kernel<C, decltype(zero)><<<grid, 64 * C::NW, 0, stream>>>(g, tm, tn);
+    });
 }
 
 template <int MT>
@@ -680,15 +722,18 @@ hipError_t launch_rows(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     constexpr int NW = 16;
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.T + MT * 16 - 1) / (MT * 16)));
-    gemm_rows_kernel<MT, NW><<<grid, 64 * NW, 0, stream>>>(g, out_dtype);
-    return hipGetLastError();
+    return with_type(out_dtype, [&](auto zero) {
+        gemm_rows_kernel<decltype(zero), MT, NW><<<grid, 64 * NW, 0, stream>>>(g);
+    });
 }
 
 template <int TC, int NW, int R>
 hipError_t launch_stream(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
-    gemm_stream_kernel<TC, NW, R><<<(unsigned)((g.N + 15) / 16), 64 * NW, 0, stream>>>(g, out_dtype);
-    return hipGetLastError();
+    return with_type(out_dtype, [&](auto zero) {
+        gemm_stream_kernel<decltype(zero), TC, NW, R>
+            <<<(unsigned)((g.N + 15) / 16), 64 * NW, 0, stream>>>(g);
+    });
 }
 
 bool aligned16(const GemmArgs &g)
