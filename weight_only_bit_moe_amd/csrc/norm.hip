@@ -66,12 +66,25 @@ __device__ __forceinline__ void store8(T *p, int left, const float (&f)[8])
     }
 }
 
+// rint(f * mult) as bytes.  Adding 1.5 * 2^23 to a float of magnitude below
+// 2^22 rounds it to an integer (nearest even, as rint does) that the low bits
+// then hold in two's complement; two permutes a pair of bytes pack them.
 __device__ __forceinline__ void store_codes(int8_t *p, int left, const float (&f)[8], float mult)
 {
-    uint32_t w[2] = {0u, 0u};
+    uint32_t b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        w[j >> 2] |= ((uint32_t)(int)__builtin_rintf(f[j] * mult) & 0xffu) << (8 * (j & 3));
+    for (int j = 0; j < 8; ++j) {
+        float v = f[j] * mult;
+        asm("" : "+v"(v));      // two roundings: not to be fused into one
+        b[j] = __float_as_uint(v + 12582912.f);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * k + 1], b[4 * k], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * k + 3], b[4 * k + 2], 0x04000c0cu);
+        w[k] = lo | hi;
+    }
     if (left >= 8) {
         *reinterpret_cast<Codes8 *>(p) = Codes8{w[0], w[1]};
     } else {
@@ -84,28 +97,23 @@ __device__ __forceinline__ void store_codes(int8_t *p, int left, const float (&f
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Sum and maximum over the workgroup's NT threads, the same on every thread.
-template <int NT>
-__device__ __forceinline__ void reduce(float &sum, uint32_t &top)
+// Sum and maximum over the workgroup (up to 16 waves), the same on every thread.
+__device__ __forceinline__ void reduce(float &sum, uint32_t &top, int waves)
 {
+    __shared__ float s[16];
+    __shared__ uint32_t t[16];
+    const int lane = threadIdx.x & 63;
     sum = wave_sum(sum);
     top = wave_max(top);
-    if constexpr (NT > 64) {
-        __shared__ float s[NT / 64];
-        __shared__ uint32_t t[NT / 64];
-        if ((threadIdx.x & 63) == 0) {
-            s[threadIdx.x >> 6] = sum;
-            t[threadIdx.x >> 6] = top;
-        }
-        __syncthreads();
-        sum = 0.f;
-        top = 0u;
-#pragma unroll
-        for (int i = 0; i < NT / 64; ++i) {
-            sum += s[i];
-            top = larger(top, t[i]);
-        }
+    if (waves == 1)
+        return;
+    if (lane == 0) {
+        s[threadIdx.x >> 6] = sum;
+        t[threadIdx.x >> 6] = top;
     }
+    __syncthreads();
+    sum = row_sum(lane < waves ? s[lane & 15] : 0.f);
+    top = row_max(lane < waves ? t[lane & 15] : 0u);
 }
 
 constexpr uint32_t kInfBits = 0x7f800000u;
@@ -123,10 +131,11 @@ __device__ __forceinline__ float code_scale(uint32_t top, float rstd)
     return top < kTinyBits ? 0.f : __uint_as_float(top) * rstd / 127.f;
 }
 
-// NT threads own one row, R chunks of 8 elements each.
-template <class T, int NT, int R>
-__global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
+// The workgroup owns a row, R chunks of 8 elements a thread.
+template <class T, int R>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a)
 {
+    const int NT = a.threads;
     const int row = blockIdx.x;
     const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
     const T *w = static_cast<const T *>(a.weight);
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
             top = larger(top, magnitude(h[i][j]));
         }
     }
-    reduce<NT>(sum, top);
+    reduce(sum, top, NT >> 6);
     const float rstd = 1.f / sqrtf(sum / (float)a.H + a.eps);
     if (a.y) {
         T *o = static_cast<T *>(a.y) + at;
@@ -216,23 +225,27 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_kernel(NormArgs a)
     }
 }
 
-// exp(-x) to about 2 ulp: x * log2(e) is split so that its rounding error,
-// which a large |x| would blow up, goes into a second exponential's linear term.
-__device__ __forceinline__ float exp_neg(float x)
+// sigmoid(x) to about 4 ulp.  exp(-x) = 2^t (1 + e ln 2): t = -x log2(e) rounded,
+// and e its rounding error, which a large |x| would otherwise blow up.  Beyond
+// 10^4 the result is 0 or 1 either way; the limit keeps e finite.
+__device__ __forceinline__ float sigmoid(float x)
 {
     constexpr float kLog2e = 1.44269502e+0f, kLow = 1.92596303e-8f, kLn2 = 0.693147181f;
+    x = __builtin_amdgcn_fmed3f(x, -1e4f, 1e4f);
     const float t = -x * kLog2e;
-    const float e = __builtin_fmaf(-x, kLog2e, -t) - x * kLow;
-    const float p = __builtin_amdgcn_exp2f(t);
-    return p > 0.f && p < INFINITY ? __builtin_fmaf(p, e * kLn2, p) : p;
+    const float e = __builtin_fmaf(-x, kLow, __builtin_fmaf(-x, kLog2e, -t));
+    const float p = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(e, kLn2, 1.f);
+    return __builtin_amdgcn_rcpf(1.f + p);          // the hardware reciprocal (1 ulp; 1 / inf = 0)
 }
 
-template <class T, int NT, int R>
-__global__ void __launch_bounds__(NT) swiglu_quant_kernel(SwigluArgs a)
+template <class T, int R>
+__global__ void __launch_bounds__(1024) swiglu_quant_kernel(SwigluArgs a)
 {
+    const int NT = a.threads;
     const int row = blockIdx.x;
     const T *g = static_cast<const T *>(a.gu) + row * a.gu_stride;
     const T *u = g + a.I;
+    const bool clamped = a.clamp < INFINITY;
     float v[R][8], f[R][8];
     float sum = 0.f;
     uint32_t top = 0u;
@@ -244,20 +257,20 @@ __global__ void __launch_bounds__(NT) swiglu_quant_kernel(SwigluArgs a)
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int left = a.I - (i * NT + (int)threadIdx.x) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // comparisons that keep a NaN (fminf would drop it)
-            const float gc = v[i][j] > a.clamp ? a.clamp : v[i][j];
-            float uc = f[i][j] > a.clamp ? a.clamp : f[i][j];
-            uc = uc < -a.clamp ? -a.clamp : uc;
-            // the hardware reciprocal (1 ulp; 1 / inf = 0)
-            const float s = __builtin_amdgcn_rcpf(1.f + exp_neg(a.alpha * gc));
-            v[i][j] = j < left ? gc * s * (uc + a.beta) : 0.f;
+            float gc = v[i][j], uc = f[i][j];
+            if (clamped) {      // comparisons that keep a NaN (fminf would drop it)
+                gc = gc > a.clamp ? a.clamp : gc;
+                uc = uc > a.clamp ? a.clamp : uc;
+                uc = uc < -a.clamp ? -a.clamp : uc;
+            }
+            // past the row's end gate and up are 0, and so is the result
+            v[i][j] = gc * sigmoid(a.alpha * gc) * (uc + a.beta);
             top = larger(top, magnitude(v[i][j]));
         }
     }
-    reduce<NT>(sum, top);
+    reduce(sum, top, NT >> 6);
     const float mult = code_mult(top);
     int8_t *o = a.q + row * a.q_stride;
 #pragma unroll
@@ -274,55 +287,51 @@ __global__ void __launch_bounds__(NT) swiglu_quant_kernel(SwigluArgs a)
         a.scale[row] = code_scale(top, 1.f);
 }
 
-// Threads and chunks per thread for rows of n elements: the fewest threads
-// that hold the row with two chunks each, up to 1024 threads, then more chunks.
+// Threads and chunks a thread for rows of n elements: one chunk a thread up to
+// 1024 threads.  More waves with less each keep more loads in flight: T = 8192,
+// H = 4096 takes 57 us with one chunk a thread, 63 us with two, 71 us with four.
 template <class F>
 hipError_t with_shape(int n, F &&f)
 {
     const int chunks = (n + 7) / 8;
-    using std::integral_constant;
-    if (chunks <= 64)
-        f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (chunks <= 128)
-        f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (chunks <= 256)
-        f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-    else if (chunks <= 512)
-        f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (chunks <= 1024)
-        f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    if (chunks <= 1024)
+        f((chunks + 63) / 64 * 64, std::integral_constant<int, 1>{});
     else if (chunks <= 2048)
-        f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+        f(1024, std::integral_constant<int, 2>{});
     else
-        f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+        f(1024, std::integral_constant<int, 4>{});
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_add_rmsnorm(const NormArgs &a, int dtype, hipStream_t stream)
+hipError_t launch_add_rmsnorm(const NormArgs &args, int dtype, hipStream_t stream)
 {
-    return with_shape(a.H, [&](auto nt, auto r) {
-        constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+    return with_shape(args.H, [&](int nt, auto r) {
+        NormArgs a = args;
+        a.threads = nt;
+        constexpr int R = decltype(r)::value;
         if (dtype == MOE_WNA16_BF16)
-            add_rmsnorm_kernel<Bf16, NT, R><<<a.T, NT, 0, stream>>>(a);
+            add_rmsnorm_kernel<Bf16, R><<<a.T, nt, 0, stream>>>(a);
         else if (dtype == MOE_WNA16_FP16)
-            add_rmsnorm_kernel<Fp16, NT, R><<<a.T, NT, 0, stream>>>(a);
+            add_rmsnorm_kernel<Fp16, R><<<a.T, nt, 0, stream>>>(a);
         else
-            add_rmsnorm_kernel<float, NT, R><<<a.T, NT, 0, stream>>>(a);
+            add_rmsnorm_kernel<float, R><<<a.T, nt, 0, stream>>>(a);
     });
 }
 
-hipError_t launch_swiglu_quant(const SwigluArgs &a, int dtype, hipStream_t stream)
+hipError_t launch_swiglu_quant(const SwigluArgs &args, int dtype, hipStream_t stream)
 {
-    return with_shape(a.I, [&](auto nt, auto r) {
-        constexpr int NT = decltype(nt)::value, R = decltype(r)::value;
+    return with_shape(args.I, [&](int nt, auto r) {
+        SwigluArgs a = args;
+        a.threads = nt;
+        constexpr int R = decltype(r)::value;
         if (dtype == MOE_WNA16_BF16)
-            swiglu_quant_kernel<Bf16, NT, R><<<a.T, NT, 0, stream>>>(a);
+            swiglu_quant_kernel<Bf16, R><<<a.T, nt, 0, stream>>>(a);
         else if (dtype == MOE_WNA16_FP16)
-            swiglu_quant_kernel<Fp16, NT, R><<<a.T, NT, 0, stream>>>(a);
+            swiglu_quant_kernel<Fp16, R><<<a.T, nt, 0, stream>>>(a);
         else
-            swiglu_quant_kernel<float, NT, R><<<a.T, NT, 0, stream>>>(a);
+            swiglu_quant_kernel<float, R><<<a.T, nt, 0, stream>>>(a);
     });
 }
 

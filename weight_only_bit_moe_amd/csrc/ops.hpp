@@ -16,6 +16,7 @@ struct NormArgs {
     const void *x, *residual, *weight;          // residual may be null
     long long x_stride, r_stride, q_stride;     // elements between rows
     int T, H;
+    int threads;                                // a row's, set by the launch
     float eps;
     void *residual_out, *y;                     // null: not written
     int8_t *q;                                  // null: no 8-bit output
@@ -29,6 +30,7 @@ struct SwigluArgs {
     const void *gu;                             // [T] rows of 2I: gate, then up
     long long gu_stride, q_stride;
     int T, I;
+    int threads;                                // a row's, set by the launch
     float alpha, beta, clamp;                   // clamp = +inf: none
     int8_t *q;
     float *scale;

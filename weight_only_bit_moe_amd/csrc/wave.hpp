@@ -86,14 +86,32 @@ __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > 
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 
-// Over the wave, the same on every lane.  All 64 lanes must be active.
+// Over the rows of 16 lanes, the first row's result on every lane; then over
+// the wave.  All 64 lanes must be active.
 template <class C>
-__device__ __forceinline__ C wave_max(C v)
+__device__ __forceinline__ C each_row_max(C v)
 {
     v = larger(v, dpp<kXor1>(v));
     v = larger(v, dpp<kXor2>(v));
     v = larger(v, dpp<kHalfMirror>(v));
-    v = larger(v, dpp<kMirror>(v));
+    return larger(v, dpp<kMirror>(v));
+}
+template <class C>
+__device__ __forceinline__ C each_row_sum(C v)
+{
+    v += dpp<kXor1>(v);
+    v += dpp<kXor2>(v);
+    v += dpp<kHalfMirror>(v);
+    return v + dpp<kMirror>(v);
+}
+template <class C>
+__device__ __forceinline__ C row_max(C v) { return lane_value(each_row_max(v), 0); }
+template <class C>
+__device__ __forceinline__ C row_sum(C v) { return lane_value(each_row_sum(v), 0); }
+template <class C>
+__device__ __forceinline__ C wave_max(C v)
+{
+    v = each_row_max(v);
     if constexpr (std::is_same<C, uint32_t>::value) {
         // kept in scalar registers: what follows is then scalar too
         uint32_t a = larger(lane_value(v, 0), lane_value(v, 16));
@@ -109,10 +127,7 @@ __device__ __forceinline__ C wave_max(C v)
 template <class C>
 __device__ __forceinline__ C wave_sum(C v)
 {
-    v += dpp<kXor1>(v);
-    v += dpp<kXor2>(v);
-    v += dpp<kHalfMirror>(v);
-    v += dpp<kMirror>(v);
+    v = each_row_sum(v);
     return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
