@@ -398,7 +398,7 @@ typedef enum {
  *   q_out        [T, H] int8, rows q_stride apart, or NULL; with it
  *   scale_out    [T] float32
  * At least one of y_out and q_out.  Tensors aligned to their element size.
- * T >= 0 (T = 0: no launch), 1 <= H <= 32768, strides >= H, eps >= 0 finite.
+ * 0 <= T <= 2^21 (T = 0: no launch), 1 <= H <= 32768, strides >= H, eps >= 0 finite.
  * A row with a NaN or infinity in v gets zero codes and a NaN scale; a row
  * with m < 2^-100 gets zero codes and scale 0.
  */
@@ -426,7 +426,7 @@ int moe_wna16_add_rmsnorm(const void *x, const void *residual, const void *weigh
  *   logits  [T, E] of dtype, rows `stride` apart
  *   bias    [E] float32, or NULL
  *   ids_out [T, topk] int32;  w_out [T, topk] float32
- * T >= 0 (T = 0: no launch), 1 <= E <= 1024, 1 <= topk <= min(E, 64),
+ * 0 <= T <= 2^21 (T = 0: no launch), 1 <= E <= 1024, 1 <= topk <= min(E, 64),
  * 1 <= groups <= 64 dividing E, 1 <= topk_groups <= groups, scale finite.
  */
 int moe_wna16_route_topk(const void *logits, const float *bias, int T, int E, int64_t stride,
@@ -469,7 +469,7 @@ int moe_wna16_gemm_w8a8(const int8_t *a, const float *a_scale, const int8_t *w,
  *
  *   gu     [T, 2I] of dtype, rows gu_stride apart
  *   q_out  [T, I] int8, rows q_stride apart;  scale_out [T] float32
- * T >= 0, 1 <= I <= 32768, strides >= the row's length; alpha, beta, clamp as
+ * 0 <= T <= 2^21, 1 <= I <= 32768, strides >= the row's length; alpha, beta, clamp as
  * in moe_wna16_forward.  Non-finite and vanishing rows as in
  * moe_wna16_add_rmsnorm.
  */

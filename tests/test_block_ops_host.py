@@ -52,6 +52,9 @@ def test_valid_arguments_reach_the_device_check(name):
     ("norm", dict(xs=63), Bd.EINVAL), ("norm", dict(rs=63), Bd.EINVAL), ("norm", dict(qs=1), Bd.EINVAL),
     ("norm", dict(rs=0, residual=None), None), ("norm", dict(qs=0, q=None), None),
     ("norm", dict(H=32769, xs=32769, rs=32769, qs=32769), Bd.EUNSUPPORTED),
+    ("norm", dict(T=(1 << 21) + 1), Bd.EUNSUPPORTED), ("norm", dict(T=1 << 21), None),
+    ("route", dict(T=(1 << 21) + 1), Bd.EUNSUPPORTED),
+    ("swiglu", dict(T=(1 << 21) + 1), Bd.EUNSUPPORTED),
     ("norm", dict(x=0), Bd.EINVAL), ("norm", dict(weight=0), Bd.EINVAL),
     ("norm", dict(y=0, q=0), Bd.EINVAL), ("norm", dict(s=0), Bd.EINVAL),
     ("norm", dict(q=0, s=0), None), ("norm", dict(ro=0), None), ("norm", dict(y=0), None),

@@ -280,6 +280,30 @@ def test_route_masked_and_non_finite(dev, score, groups, kg):
     ids, w = M.route_topk(logits[8:].to(dev), k, bias=out.to(dev), score=score)
     check_route(logits[8:], k, ids, w, out, score)
     assert int(ids[0, 0]) == 3 and bool((ids % 2 == 1).all())
+    many = torch.zeros(256)                           # experts that are always on, all equal
+    many[[5, 70, 71, 133, 200, 202, 255]] = INF
+    wide = torch.randn(9, 256, generator=g)
+    for gr, kgr in ((1, 1), (8, 3), (4, 4)):
+        ids, w = M.route_topk(wide.to(dev), k, bias=many.to(dev), score=score, groups=gr,
+                              topk_groups=kgr)
+        check_route(wide, k, ids, w, many, score, gr, kgr)
+
+
+@pytest.mark.parametrize("E", [128, 256, 1000])
+def test_route_negative_and_equal_scores(dev, E):
+    """A bias below zero turns the scores negative; a constant one leaves ties and zeros."""
+    g = gen("negative", E)
+    logits = torch.randn(40, E, generator=g)
+    logits[:, ::7] = logits[:, :1]
+    for bias in (torch.randn(E, generator=g) - 2, torch.full((E,), -0.5), -torch.rand(E, generator=g) * 1e4):
+        for score in ("softmax", "sigmoid"):
+            ids, w = M.route_topk(logits.to(dev), 7, bias=bias.to(dev), score=score)
+            check_route(logits, 7, ids, w, bias, score)
+    flat = torch.zeros(3, E)
+    flat[1] = -0.0
+    flat[2, ::2] = -0.0                               # -0 and +0 are one logit
+    ids, w = M.route_topk(flat.to(dev), 9)
+    check_route(flat, 9, ids, w)
 
 
 def test_route_strided_rows(dev):

@@ -33,7 +33,7 @@ int moe_wna16_add_rmsnorm(const void *x, const void *residual, const void *weigh
 {
     if (T < 0 || H <= 0 || !valid_dtype(dtype) || !std::isfinite(eps) || eps < 0.f)
         return MOE_WNA16_EINVAL;
-    if (H > wna16::kMaxRow)
+    if (H > wna16::kMaxRow || T > wna16::kMaxRows)
         return MOE_WNA16_EUNSUPPORTED;
     if (x_stride < H || (residual && r_stride < H) || (q_out && q_stride < H))
         return MOE_WNA16_EINVAL;
@@ -75,7 +75,7 @@ int moe_wna16_route_topk(const void *logits, const float *bias, int T, int E, in
         E % groups != 0 || topk_groups <= 0 || topk_groups > groups || stride < E ||
         !std::isfinite(scale))
         return MOE_WNA16_EINVAL;
-    if (E > 1024 || topk > 64 || groups > 64)
+    if (E > 1024 || topk > 64 || groups > 64 || T > wna16::kMaxRows)
         return MOE_WNA16_EUNSUPPORTED;
     if (T == 0)
         return MOE_WNA16_OK;
@@ -181,7 +181,7 @@ int moe_wna16_swiglu_quant(const void *gu, int T, int I, int64_t gu_stride, int 
     if (T < 0 || I <= 0 || !valid_dtype(dtype) || !std::isfinite(alpha) || !std::isfinite(beta) ||
         std::isnan(clamp) || !(clamp > 0.f) || gu_stride < 2ll * I || q_stride < I)
         return MOE_WNA16_EINVAL;
-    if (I > wna16::kMaxRow)
+    if (I > wna16::kMaxRow || T > wna16::kMaxRows)
         return MOE_WNA16_EUNSUPPORTED;
     if (T == 0)
         return MOE_WNA16_OK;

@@ -694,17 +694,15 @@ gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
                        (slice + 1) * chunks / g.split, id, slice, lds);
 }
 
-// f(a value of the output type), then the launch's status.
+// f(a value of the output type).
 template <class F>
 hipError_t with_type(int out_dtype, F &&f)
 {
     if (out_dtype == MOE_WNA16_BF16)
-        f(Bf16{});
-    else if (out_dtype == MOE_WNA16_FP16)
-        f(Fp16{});
-    else
-        f(0.f);
-    return hipGetLastError();
+        return f(Bf16{});
+    if (out_dtype == MOE_WNA16_FP16)
+        return f(Fp16{});
+    return f(0.f);
 }
 
 template <class C>
@@ -713,7 +711,7 @@ hipError_t launch_tile(const GemmArgs &g, int out_dtype, hipStream_t stream)
     const int tm = (g.T + C::BM - 1) / C::BM, tn = (g.N + C::BN - 1) / C::BN;
     const unsigned grid = (unsigned)((tm * tn * g.split + 7) / 8 * 8);
     return with_type(out_dtype, [&](auto zero) {
-        gemm_tile_kernel<C, decltype(zero)><<<grid, 64 * C::NW, 0, stream>>>(g, tm, tn);
+        return launch(gemm_tile_kernel<C, decltype(zero)>, dim3(grid), 64 * C::NW, stream, g, tm, tn);
     });
 }
 
@@ -723,7 +721,7 @@ hipError_t launch_rows(const GemmArgs &g, int out_dtype, hipStream_t stream)
     constexpr int NW = 16;
     const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.T + MT * 16 - 1) / (MT * 16)));
     return with_type(out_dtype, [&](auto zero) {
-        gemm_rows_kernel<decltype(zero), MT, NW><<<grid, 64 * NW, 0, stream>>>(g);
+        return launch(gemm_rows_kernel<decltype(zero), MT, NW>, grid, 64 * NW, stream, g);
     });
 }
 
@@ -731,8 +729,8 @@ template <int TC, int NW, int R>
 hipError_t launch_stream(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     return with_type(out_dtype, [&](auto zero) {
-        gemm_stream_kernel<decltype(zero), TC, NW, R>
-            <<<(unsigned)((g.N + 15) / 16), 64 * NW, 0, stream>>>(g);
+        return launch(gemm_stream_kernel<decltype(zero), TC, NW, R>,
+                      dim3((unsigned)((g.N + 15) / 16)), 64 * NW, stream, g);
     });
 }
 

@@ -295,12 +295,10 @@ hipError_t with_shape(int n, F &&f)
 {
     const int chunks = (n + 7) / 8;
     if (chunks <= 1024)
-        f((chunks + 63) / 64 * 64, std::integral_constant<int, 1>{});
-    else if (chunks <= 2048)
-        f(1024, std::integral_constant<int, 2>{});
-    else
-        f(1024, std::integral_constant<int, 4>{});
-    return hipGetLastError();
+        return f((chunks + 63) / 64 * 64, std::integral_constant<int, 1>{});
+    if (chunks <= 2048)
+        return f(1024, std::integral_constant<int, 2>{});
+    return f(1024, std::integral_constant<int, 4>{});
 }
 
 }  // namespace
@@ -312,11 +310,10 @@ hipError_t launch_add_rmsnorm(const NormArgs &args, int dtype, hipStream_t strea
         a.threads = nt;
         constexpr int R = decltype(r)::value;
         if (dtype == MOE_WNA16_BF16)
-            add_rmsnorm_kernel<Bf16, R><<<a.T, nt, 0, stream>>>(a);
-        else if (dtype == MOE_WNA16_FP16)
-            add_rmsnorm_kernel<Fp16, R><<<a.T, nt, 0, stream>>>(a);
-        else
-            add_rmsnorm_kernel<float, R><<<a.T, nt, 0, stream>>>(a);
+            return launch(add_rmsnorm_kernel<Bf16, R>, dim3(a.T), nt, stream, a);
+        if (dtype == MOE_WNA16_FP16)
+            return launch(add_rmsnorm_kernel<Fp16, R>, dim3(a.T), nt, stream, a);
+        return launch(add_rmsnorm_kernel<float, R>, dim3(a.T), nt, stream, a);
     });
 }
 
@@ -327,11 +324,10 @@ hipError_t launch_swiglu_quant(const SwigluArgs &args, int dtype, hipStream_t st
         a.threads = nt;
         constexpr int R = decltype(r)::value;
         if (dtype == MOE_WNA16_BF16)
-            swiglu_quant_kernel<Bf16, R><<<a.T, nt, 0, stream>>>(a);
-        else if (dtype == MOE_WNA16_FP16)
-            swiglu_quant_kernel<Fp16, R><<<a.T, nt, 0, stream>>>(a);
-        else
-            swiglu_quant_kernel<float, R><<<a.T, nt, 0, stream>>>(a);
+            return launch(swiglu_quant_kernel<Bf16, R>, dim3(a.T), nt, stream, a);
+        if (dtype == MOE_WNA16_FP16)
+            return launch(swiglu_quant_kernel<Fp16, R>, dim3(a.T), nt, stream, a);
+        return launch(swiglu_quant_kernel<float, R>, dim3(a.T), nt, stream, a);
     });
 }
 

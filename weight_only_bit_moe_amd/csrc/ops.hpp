@@ -25,6 +25,7 @@ struct NormArgs {
 // dtype: moe_wna16_dtype of x, residual, weight, residual_out and y.
 hipError_t launch_add_rmsnorm(const NormArgs &a, int dtype, hipStream_t stream);
 constexpr int kMaxRow = 32768;                  // longest row of the row kernels
+constexpr int kMaxRows = 1 << 21;               // a launch stays below 2^32 threads
 
 struct SwigluArgs {
     const void *gu;                             // [T] rows of 2I: gate, then up

@@ -124,7 +124,8 @@ template <bool SOFTMAX> constexpr float kScoreError = (SOFTMAX ? 31 : 5) * 0x1p-
 
 __device__ __forceinline__ bool too_near(float a, float b, float tolerance)
 {
-    return __builtin_fabsf(a - b) <= tolerance * (1.f + __builtin_fabsf(b));
+    // two infinities differ by a NaN: too near as well
+    return !(__builtin_fabsf(a - b) > tolerance * (1.f + __builtin_fabsf(b)));
 }
 
 // Takes the experts outside the best groups out of c.  Returns whether two
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
 }
 
 template <class T, bool SOFTMAX>
-void launch_epl(const RouteArgs &a, hipStream_t stream)
+hipError_t launch_epl(const RouteArgs &a, hipStream_t stream)
 {
     const unsigned grid = (unsigned)((a.T + kWaves - 1) / kWaves);
     auto go = [&](auto n) {
@@ -478,21 +479,19 @@ void launch_epl(const RouteArgs &a, hipStream_t stream)
                      ? span
                      : 0;
         if (a.bias || a.groups > 1)
-            route_topk_kernel<T, EPL, SOFTMAX, true><<<grid, 64 * kWaves, 0, stream>>>(b);
-        else
-            route_topk_kernel<T, EPL, SOFTMAX, false><<<grid, 64 * kWaves, 0, stream>>>(b);
+            return launch(route_topk_kernel<T, EPL, SOFTMAX, true>, dim3(grid), 64 * kWaves, stream, b);
+        return launch(route_topk_kernel<T, EPL, SOFTMAX, false>, dim3(grid), 64 * kWaves, stream, b);
     };
     const int epl = (a.E + 63) / 64;
     if (epl <= 1)
-        go(std::integral_constant<int, 1>{});
-    else if (epl <= 2)
-        go(std::integral_constant<int, 2>{});
-    else if (epl <= 4)
-        go(std::integral_constant<int, 4>{});
-    else if (epl <= 8)
-        go(std::integral_constant<int, 8>{});
-    else
-        go(std::integral_constant<int, 16>{});
+        return go(std::integral_constant<int, 1>{});
+    if (epl <= 2)
+        return go(std::integral_constant<int, 2>{});
+    if (epl <= 4)
+        return go(std::integral_constant<int, 4>{});
+    if (epl <= 8)
+        return go(std::integral_constant<int, 8>{});
+    return go(std::integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -501,12 +500,10 @@ hipError_t launch_route_topk(const RouteArgs &a, int dtype, int score, hipStream
 {
     const bool softmax = score == MOE_WNA16_SOFTMAX;
     if (dtype == MOE_WNA16_BF16)
-        softmax ? launch_epl<Bf16, true>(a, stream) : launch_epl<Bf16, false>(a, stream);
-    else if (dtype == MOE_WNA16_FP16)
-        softmax ? launch_epl<Fp16, true>(a, stream) : launch_epl<Fp16, false>(a, stream);
-    else
-        softmax ? launch_epl<float, true>(a, stream) : launch_epl<float, false>(a, stream);
-    return hipGetLastError();
+        return softmax ? launch_epl<Bf16, true>(a, stream) : launch_epl<Bf16, false>(a, stream);
+    if (dtype == MOE_WNA16_FP16)
+        return softmax ? launch_epl<Fp16, true>(a, stream) : launch_epl<Fp16, false>(a, stream);
+    return softmax ? launch_epl<float, true>(a, stream) : launch_epl<float, false>(a, stream);
 }
 
 }  // namespace wna16

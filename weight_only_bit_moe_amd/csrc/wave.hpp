@@ -1,4 +1,5 @@
-// Element types and wave-wide reductions shared by the operators' kernels.
+// Element types, wave-wide reductions and the launch shared by the operators'
+// kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -129,6 +130,16 @@ __device__ __forceinline__ C wave_sum(C v)
 {
     v = each_row_sum(v);
     return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// Launches kernel(args...), and returns this launch's own status: an error that
+// an earlier call on the thread left behind is neither reported nor cleared.
+template <class... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, hipStream_t stream, P... args)
+{
+    void *p[] = {&args...};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, dim3((unsigned)threads), p,
+                           0, stream);
 }
 
 }  // namespace
