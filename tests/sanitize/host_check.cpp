@@ -255,9 +255,81 @@ static void check_oracle()
                    oracle_f64_to_f16_rne(v)), "fp16 round trip");
 }
 
+// The operators around the layer: refusals, and the product's plans over many
+// shapes through its workspace size.
+static void check_block_ops()
+{
+    auto *f = static_cast<float *>(fake());
+    auto *b = static_cast<int8_t *>(fake());
+    auto *i = static_cast<int32_t *>(fake());
+    const float inf = INFINITY;
+    auto norm = [&](int T, int H, int64_t xs, int dtype, float eps, const void *x, int8_t *q,
+                    float *scale) {
+        return moe_wna16_add_rmsnorm(x, fake(), fake(), T, H, xs, H, dtype, eps, fake(), nullptr, q,
+                                     H, scale, nullptr);
+    };
+    EXPECT(norm(-1, 64, 64, 0, 0.f, f, b, f) == MOE_WNA16_EINVAL, "norm T");
+    EXPECT(norm(4, 0, 64, 0, 0.f, f, b, f) == MOE_WNA16_EINVAL, "norm H");
+    EXPECT(norm(4, 64, 63, 0, 0.f, f, b, f) == MOE_WNA16_EINVAL, "norm stride");
+    EXPECT(norm(4, 64, 64, 3, 0.f, f, b, f) == MOE_WNA16_EINVAL, "norm type");
+    EXPECT(norm(4, 64, 64, 0, NAN, f, b, f) == MOE_WNA16_EINVAL, "norm eps");
+    EXPECT(norm(4, 64, 64, 0, 0.f, nullptr, b, f) == MOE_WNA16_EINVAL, "norm null");
+    EXPECT(norm(4, 64, 64, 0, 0.f, f, nullptr, f) == MOE_WNA16_EINVAL, "norm without an output");
+    EXPECT(norm(4, 64, 64, 0, 0.f, f, b, nullptr) == MOE_WNA16_EINVAL, "norm codes without scales");
+    EXPECT(norm(4, 64, 64, 2, 0.f, fake(2), b, f) == MOE_WNA16_EALIGN, "norm alignment");
+    EXPECT(norm(4, 40000, 40000, 0, 0.f, f, b, f) == MOE_WNA16_EUNSUPPORTED, "norm row");
+    EXPECT(norm(0, 64, 64, 0, 0.f, nullptr, nullptr, nullptr) == MOE_WNA16_OK, "norm empty");
+    auto route = [&](int T, int E, int k, int score, int groups, int kg, float scale, int32_t *ids) {
+        return moe_wna16_route_topk(f, f, T, E, E, 2, k, score, groups, kg, 1, scale, ids, f, nullptr);
+    };
+    EXPECT(route(4, 64, 65, 0, 1, 1, 1.f, i) == MOE_WNA16_EINVAL, "route topk");
+    EXPECT(route(4, 64, 6, 2, 1, 1, 1.f, i) == MOE_WNA16_EINVAL, "route score");
+    EXPECT(route(4, 64, 6, 0, 7, 1, 1.f, i) == MOE_WNA16_EINVAL, "route groups");
+    EXPECT(route(4, 64, 6, 0, 8, 9, 1.f, i) == MOE_WNA16_EINVAL, "route topk_groups");
+    EXPECT(route(4, 64, 6, 0, 8, 4, inf, i) == MOE_WNA16_EINVAL, "route scale");
+    EXPECT(route(4, 2048, 6, 0, 8, 4, 1.f, i) == MOE_WNA16_EUNSUPPORTED, "route experts");
+    EXPECT(route(4, 64, 6, 0, 8, 4, 1.f, nullptr) == MOE_WNA16_EINVAL, "route null");
+    EXPECT(route(0, 64, 6, 0, 8, 4, 1.f, nullptr) == MOE_WNA16_OK, "route empty");
+    auto gemm = [&](int T, int N, int K, int64_t lda, const void *out, void *ws, size_t bytes) {
+        return moe_wna16_gemm_w8a8(b, f, b, f, nullptr, T, N, K, lda, K, 0, N, 0,
+                                   const_cast<void *>(out), ws, bytes, nullptr);
+    };
+    EXPECT(gemm(4, 64, 0, 64, f, nullptr, 0) == MOE_WNA16_EINVAL, "product K");
+    EXPECT(gemm(4, 64, 131072, 131072, f, nullptr, 0) == MOE_WNA16_EUNSUPPORTED, "product long K");
+    EXPECT(gemm(4, 64, 64, 63, f, nullptr, 0) == MOE_WNA16_EINVAL, "product stride");
+    EXPECT(gemm(4, 64, 64, 64, nullptr, nullptr, 0) == MOE_WNA16_EINVAL, "product null");
+    EXPECT(gemm(4, 64, 64, 64, fake(1), nullptr, 0) == MOE_WNA16_EALIGN, "product alignment");
+    EXPECT(gemm(0, 64, 64, 64, nullptr, nullptr, 0) == MOE_WNA16_OK, "product empty");
+    size_t bytes = 0;
+    EXPECT(moe_wna16_gemm_w8a8_workspace_size(4, 64, 64, nullptr) == MOE_WNA16_EINVAL, "size null");
+    int split = 0;
+    for (int T : {1, 64, 65, 128, 300, 2047, 8192, 1 << 21})
+        for (int N : {1, 16, 512, 2056, 4096, 1 << 21})
+            for (int K : {1, 128, 4096, 16384, 131071}) {
+                EXPECT(moe_wna16_gemm_w8a8_workspace_size(T, N, K, &bytes) == MOE_WNA16_OK, "size");
+                if (bytes) {
+                    ++split;
+                    EXPECT(bytes > MOE_WNA16_GEMM_SYNC_BYTES && bytes < ((size_t)1 << 28), "size");
+                    EXPECT(gemm(T, N, K, K, f, nullptr, bytes) == MOE_WNA16_EINVAL, "workspace null");
+                    EXPECT(gemm(T, N, K, K, f, fake(), bytes - 1) == MOE_WNA16_EWORKSPACE, "workspace");
+                    EXPECT(gemm(T, N, K, K, f, fake(16), bytes) == MOE_WNA16_EALIGN, "workspace align");
+                }
+            }
+    EXPECT(split > 0, "some products split K");
+    auto swiglu = [&](int T, int I, int64_t ld, float clamp, const void *gu) {
+        return moe_wna16_swiglu_quant(gu, T, I, ld, 0, 1.f, 0.f, clamp, b, I, f, nullptr);
+    };
+    EXPECT(swiglu(4, 64, 127, inf, f) == MOE_WNA16_EINVAL, "swiglu stride");
+    EXPECT(swiglu(4, 64, 128, 0.f, f) == MOE_WNA16_EINVAL, "swiglu clamp");
+    EXPECT(swiglu(4, 64, 128, inf, nullptr) == MOE_WNA16_EINVAL, "swiglu null");
+    EXPECT(swiglu(4, 64, 128, inf, fake(1)) == MOE_WNA16_EALIGN, "swiglu alignment");
+    EXPECT(swiglu(0, 64, 128, inf, nullptr) == MOE_WNA16_OK, "swiglu empty");
+}
+
 int main()
 {
     check_abi();
+    check_block_ops();
     check_oracle();
     if (failures) {
         std::fprintf(stderr, "%d host check(s) failed\n", failures);

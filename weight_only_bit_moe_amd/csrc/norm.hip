@@ -4,7 +4,11 @@
 // Both are one pass over memory: a workgroup owns a row, every thread keeps
 // its share of the row in registers between the reduction and the output, so
 // each input is read once and each output written once.  They are bound by
-// HBM for many rows and by the launch and one memory round trip for few.
+// HBM for many rows and by the launch and one memory round trip for few:
+//   norm, bf16, H = 4096, residual, 16- and 8-bit outputs:
+//     T = 8192  57 us = 5.3 TB/s;  T = 2048  15.1 us = 5.0 TB/s;  T = 4  3.8 us
+//   SwiGLU, bf16, I = 2048:  T = 8192  19.4 us = 4.3 TB/s;  T = 64  4 us
+// (a copy of 2 GiB runs at 4.8 TB/s).
 //
 // 8-bit rows.  With v the row before its norm's factor and m = max |v|:
 //   q = rint(v * (127 / m)),  scale = m * rstd / 127.
