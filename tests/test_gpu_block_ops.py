@@ -365,7 +365,8 @@ def test_gemm(dev, T, N, K, dt):
 
 @pytest.mark.parametrize("T,N,K", [(4200, 2050, 512), (4096, 4096, 272), (6200, 2304, 144),
                                    (2040, 2050, 4112), (4090, 4090, 1040), (1020, 4070, 2064),
-                                   (510, 4080, 2064), (250, 2000, 2064)])
+                                   (510, 4080, 2064), (250, 2000, 2064), (2040, 4090, 1040),
+                                   (2047, 2056, 400), (1900, 3000, 784)])
 def test_gemm_large_tiles(dev, T, N, K):
     a, sa, w, sw, g = operands(T, N, K, "large")
     add = torch.randn(T, N, generator=g).to(BF)

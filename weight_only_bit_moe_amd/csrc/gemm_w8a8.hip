@@ -588,8 +588,14 @@ struct Tile8 {
     {
         constexpr int ROW = WCOLS * sizeof(T), PIECES = ROW / 16, EPP = 16 / sizeof(T);
         constexpr int MP = MT < 2 ? MT : 2;   // 16-row steps a pass
-        static_assert(MT % MP == 0 && PIECES >= 4 && MP * 16 * ROW <= REGION, "passes fit");
-        auto spread = [](int row) { return PIECES >= 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
+        // rows of 4, 8 or 16 pieces are swizzled, others lie a piece further apart
+        constexpr bool kSwizzled = (PIECES & (PIECES - 1)) == 0;
+        constexpr int PITCH = kSwizzled ? ROW : ROW + 16;
+        static_assert(MT % MP == 0 && PIECES >= 4 && MP * 16 * PITCH <= REGION, "passes fit");
+        static_assert(MP * 16 * PIECES % 64 == 0, "whole stores");
+        auto spread = [](int row) {
+            return !kSwizzled ? 0 : PIECES >= 8 ? (row >> 1) & 7 : (row >> 2) & 3;
+        };
         const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
 #pragma unroll
         for (int p = 0; p < MT / MP; ++p) {
@@ -608,7 +614,7 @@ struct Tile8 {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int byte = (n * 16 + kq * 4) * (int)sizeof(T);
-                    char *at = region + row * ROW + (((byte >> 4) ^ spread(row)) << 4) +
+                    char *at = region + row * PITCH + (((byte >> 4) ^ spread(row)) << 4) +
                                (byte & 15);
                     Out4<T> v;
 #pragma unroll
@@ -631,7 +637,7 @@ struct Tile8 {
             for (int i = 0; i < STEPS; ++i) {
                 const int id = i * 64 + lane, row = id / PIECES, c = id % PIECES;
                 const int t = t0 + p * MP * 16 + row, n = n0 + c * EPP;
-                const v4i v = *reinterpret_cast<const v4i *>(region + row * ROW +
+                const v4i v = *reinterpret_cast<const v4i *>(region + row * PITCH +
                                                              ((c ^ spread(row)) << 4));
                 store_piece<T>(g, t, n, v);
             }
@@ -765,9 +771,9 @@ struct TileCost {
     float once, few, all, two, more;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 10.6f, 1.30f, 1.73f, 0.f, 8.0f}, {128, 256, 9.5f, 0.50f, 0.80f, 0.f, 10.0f},
-    {128, 128, 7.3f, 0.326f, 0.43f, 0.f, 5.5f}, {128, 64, 5.5f, 0.255f, 0.30f, 0.542f, 1.3f},
-    {64, 64, 4.8f, 0.163f, 0.19f, 0.372f, 0.2f},
+    {256, 256, 10.6f, 1.30f, 1.73f, 0.f, 8.0f}, {128, 256, 9.5f, 0.42f, 0.76f, 0.f, 10.0f},
+    {128, 192, 8.4f, 0.36f, 0.60f, 0.f, 8.0f},  {128, 128, 7.3f, 0.30f, 0.44f, 0.f, 5.5f},
+    {128, 64, 5.5f, 0.255f, 0.30f, 0.542f, 1.3f}, {64, 64, 4.8f, 0.163f, 0.19f, 0.372f, 0.2f},
 };
 constexpr int kMaxSplit = 16;
 
@@ -828,6 +834,8 @@ hipError_t launch_gemm_w8a8(const GemmArgs &g, const GemmPlan &p, int out_dtype,
             return launch_tile<Tile8<256, 256, 2, 4, 2>>(g, out_dtype, stream);
         if (p.bn == 256)
             return launch_tile<Tile8<128, 256, 2, 4, 3>>(g, out_dtype, stream);
+        if (p.bn == 192)
+            return launch_tile<Tile8<128, 192, 2, 4, 3>>(g, out_dtype, stream);
         if (p.bn == 128)
             return launch_tile<Tile8<128, 128, 2, 4, 4>>(g, out_dtype, stream);
         if (p.bm == 128)
