@@ -439,6 +439,30 @@ def test_gemm_strided_and_unaligned(dev, T, pad, offset):
     assert bool(torch.isnan(gap).all())
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 40, 1), (3, 5000, 4090), (8, 100, 15), (13, 100, 2063), (16, 4200, 777),
+                                   (27, 333, 3001), (64, 130, 2050), (64, 40, 16399),
+                                   (65, 40, 17), (100, 700, 127), (90, 300, 129), (128, 512, 4090),
+                                   (66, 20, 131071), (300, 130, 6161), (513, 384, 257), (510, 4080, 1030),
+                                   (2047, 2056, 401), (2040, 2050, 1001), (4090, 4090, 385), (4200, 2050, 523),
+                                   (6200, 2304, 133), (1020, 4070, 2063), (2040, 4090, 1039)])
+def test_gemm_odd_lengths(dev, T, N, K):
+    """K at which no row but the first begins at a multiple of 16 bytes, for every tile and split: what
+    follows a row in memory (the next row's codes) is not counted."""
+    a, sa, w, sw, g = operands(T, N, K, "odd")
+    ws = M.gemm_w8a8_workspace_for(T, N, K, dev)
+    if ws is not None:
+        ws[4096:] = 0x5A
+    add = torch.randn(T, N, generator=g).to(BF)
+    d = [v.to(dev) for v in (a, sa, w, sw)]
+    for _ in range(2):
+        out = M.gemm_w8a8(*d, addend=add.to(dev), workspace=ws)
+        check_gemm(a, sa, w, sw, add, out)
+    assert ws is None or not bool(ws[:4096].any())
+    # operands at odd addresses, and one aligned with the other not
+    o = torch.empty(T * K + 1, dtype=torch.int8, device=dev)[1:].view(T, K).copy_(a)
+    assert torch.equal(out, M.gemm_w8a8(o, *d[1:], addend=add.to(dev)))
+
+
 def test_gemm_row_offsets_past_32_bits(dev):
     T, N, K, ld = 620, 80, 160, (1 << 23) - 16
     a, sa, w, sw, _ = operands(T, N, K, "far")

@@ -11,6 +11,10 @@
 // a long run of the tile loop (K = 32768) the MFMAs are busy 72 % of the cycles,
 // at a clock that has fallen to 1.5 GHz: power bounds it, the more bits of the
 // operands change the more.  A library product of the same size takes 128 us.
+// Operands whose rows do not all begin at multiples of 16 bytes go the same ways
+// through registers (N = 4096, K = 4090 against 4096: T = 4 6.2 and 5.6 us, T = 64
+// 11.4 and 8.5 us, T = 256 16.9 and 10.6 us, T = 8192 216 and 127 us): every such
+// load touches two lines, and an LDS store follows it.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -86,17 +90,33 @@ __device__ __forceinline__ v4i load16(const int8_t *p)
     const Bytes16 b = *reinterpret_cast<const Bytes16 *>(p);
     return v4i{b.v[0], b.v[1], b.v[2], b.v[3]};
 }
-// The first `left` of 16 bytes, zeros behind them.
-__device__ __forceinline__ v4i load_tail(const int8_t *p, int left)
+// Pieces of 16 bytes of which left(i) (any number) lie before the row's end,
+// zeros behind it.  Of a piece that crosses the end the row's last 16 bytes are
+// loaded and moved down; a row of fewer bytes is read one by one.
+template <int N, class At, class Left>
+__device__ __forceinline__ void load_ends(v4i (&to)[N], At &&at, Left &&left)
 {
-    if (left >= 16)
-        return load16(p);
-    v4i r = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 15; ++i)
-        if (i < left)
-            r[i >> 2] |= (int)((uint32_t)(uint8_t)p[i] << (8 * (i & 3)));
-    return r;
+    for (int i = 0; i < N; ++i)
+        to[i] = load16(left(i) >= 16 ? at(i) : at(i) + (left(i) - 16));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int gone = 16 - left(i);
+        const unsigned __int128 u = __builtin_bit_cast(unsigned __int128, to[i]);
+        if (gone > 0)
+            to[i] = __builtin_bit_cast(v4i, gone < 16 ? u >> (8 * gone) : 0);
+    }
+}
+template <int N, class At, class Left>
+__device__ __forceinline__ void load_short(v4i (&to)[N], At &&at, Left &&left)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        unsigned __int128 u = 0;
+        for (int b = left(i) - 1; b >= 0; --b)
+            u = u << 8 | (uint8_t)at(i)[b];
+        to[i] = __builtin_bit_cast(v4i, u);
+    }
 }
 
 // LDS byte address of a __shared__ pointer.
@@ -162,18 +182,20 @@ __device__ __forceinline__ void join_waves(const GemmArgs &g, const v4i (&acc)[M
 // join.  The way through LDS is for the addresses: an MFMA wants lane l to hold
 // row l % 16, and a load in that order has every lane in another row, which the
 // address unit takes one lane a cycle; the copies take eight lanes of one row
-// in a row, four lanes a cycle.
+// in a row, four lanes a cycle.  ANY: operands at any address and any K, which
+// no such copy can fetch: R chunks of a wave are held in registers instead, and
+// pass through one stage.
 // ---------------------------------------------------------------------------
-template <class T, int TC, int NW, int R>
+template <class T, int TC, int NW, int R, bool ANY>
 __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g)
 {
     constexpr int MT = TC < 2 ? 1 : TC / 2, ROWS = 16 + 8 * TC, STAGE = ROWS * 128;
-    constexpr int COPIES = ROWS / 8, RING = NW * R * STAGE, PART = NW * MT * 1024;
+    constexpr int COPIES = ROWS / 8, RING = NW * (ANY ? 1 : R) * STAGE, PART = NW * MT * 1024;
     __shared__ __attribute__((aligned(1024))) char lds[RING > PART ? RING : PART];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16;
-    char *ring = lds + wave * (R * STAGE);
+    char *ring = lds + wave * ((ANY ? 1 : R) * STAGE);
     const uint32_t ring0 = lds_of(ring);
     // copy i brings rows [8i, 8i + 8): channels first, then tokens; rows past
     // the end repeat the last one
@@ -209,18 +231,8 @@ __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
         acc[m] = v4i{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (wave + i * NW < chunks)
-            copy(wave + i * NW, i);
-    for (int c = wave, stage = 0; c < chunks; c += NW, stage = stage + 1 == R ? 0 : stage + 1) {
-        // the copies behind this chunk's stay in flight
-        if (c + (R - 1) * NW < chunks)
-            wait_copies<(R - 1) * COPIES>();
-        else
-            wait_copies<0>();
-        const char *st = ring + stage * STAGE;
-        v4i fw[2], fa[2][MT];
+    // a chunk's products from its stage
+    auto read = [&](const char *st, v4i (&fw)[2], v4i (&fa)[2][MT]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             fw[s] = *reinterpret_cast<const v4i *>(st + r * 128 + place(r, s * 4 + kq) * 16);
@@ -231,86 +243,81 @@ __global__ void __launch_bounds__(64 * NW) gemm_stream_kernel(GemmArgs g)
                                                           place(row, s * 4 + kq) * 16);
             }
         }
-        if ((c + 1) * 128 > g.K) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (c * 128 + s * 64 + kq * 16 >= g.K)
-                    fw[s] = v4i{0, 0, 0, 0};
-        }
-        if (c + R * NW < chunks) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage has been read
-            copy(c + R * NW, stage);
-        }
+    };
+    auto multiply = [&](const v4i (&fw)[2], const v4i (&fa)[2][MT]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s], fa[s][m], acc[m], 0, 0, 0);
+    };
+    if constexpr (ANY) {
+        v4i held[R][COPIES];
+        auto load = [&](v4i (&to)[COPIES], int c) {
+            auto at = [&](int i) { return (i < 2 ? wbase : g.a) + off[i] + (uint32_t)(c * 128); };
+            auto left = [&](int i) { return g.K - c * 128 - cplace[i & 1]; };
+            if ((c + 1) * 128 <= g.K) {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    to[i] = load16(at(i));
+            } else if (g.K >= 16) {
+                load_ends(to, at, left);
+            } else {
+                load_short(to, at, left);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (wave + i * NW < chunks)
+                load(held[i], wave + i * NW);
+        for (int c0 = wave; c0 < chunks; c0 += R * NW)
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const int c = c0 + j * NW;
+                if (c >= chunks)
+                    break;
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    *reinterpret_cast<v4i *>(ring + i * 1024 + lane * 16) = held[j][i];
+                if (c + R * NW < chunks)
+                    load(held[j], c + R * NW);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                v4i fw[2], fa[2][MT];
+                read(ring, fw, fa);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                multiply(fw, fa);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (wave + i * NW < chunks)
+                copy(wave + i * NW, i);
+        for (int c = wave, stage = 0; c < chunks;
+             c += NW, stage = stage + 1 == R ? 0 : stage + 1) {
+            // the copies behind this chunk's stay in flight
+            if (c + (R - 1) * NW < chunks)
+                wait_copies<(R - 1) * COPIES>();
+            else
+                wait_copies<0>();
+            v4i fw[2], fa[2][MT];
+            read(ring + stage * STAGE, fw, fa);
+            if ((c + 1) * 128 > g.K) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (c * 128 + s * 64 + kq * 16 >= g.K)
+                        fw[s] = v4i{0, 0, 0, 0};
+            }
+            if (c + R * NW < chunks) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage has been read
+                copy(c + R * NW, stage);
+            }
+            multiply(fw, fa);
+        }
     }
     __syncthreads();                                // every ring has been read
     join_waves<T, MT, NW>(g, acc, reinterpret_cast<int *>(lds), n0, 0, beside);
-}
-
-// ---------------------------------------------------------------------------
-// Operands that no 16-byte copy can address, any number of tokens: both go from
-// memory to the MFMA's registers directly, lane l holding 16 bytes of row
-// l % 16 at K offset 16 * (l / 16).  A workgroup owns 16 channels and MT * 16
-// tokens, its waves split K.  Channels are the MFMA's rows, so a lane ends up
-// with four consecutive channels of one token and stores them at once.
-// ---------------------------------------------------------------------------
-template <class T, int MT, int NW>
-__global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g)
-{
-    __shared__ int part[NW][MT][256];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (MT * 16);
-    const int r = lane & 15, kc = (lane >> 4) * 16;
-    Beside<T> beside;
-    if (wave < MT)
-        beside.load(g, t0 + wave * 16 + r, n0 + (lane >> 4) * 4);
-    const int nr = n0 + r < g.N ? n0 + r : g.N - 1;     // rows past the end repeat the last
-    const int8_t *w = g.w + nr * g.ldw + kc;
-    const int8_t *a[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int tr = t0 + m * 16 + r;
-        a[m] = g.a + (tr < g.T ? tr : g.T - 1) * g.lda + kc;
-    }
-    v4i acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        acc[m] = v4i{0, 0, 0, 0};
-    // steps of 64 K; a wave takes runs of two (whole 128-byte lines)
-    constexpr int S = 2;
-    int k = wave * (64 * S);
-    for (; k + 64 * S <= g.K; k += NW * 64 * S) {
-        v4i fw[S], fa[S][MT];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            fw[s] = load16(w + k + s * 64);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                fa[s][m] = load16(a[m] + k + s * 64);
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s], fa[s][m], acc[m], 0, 0, 0);
-    }
-    // what is left of K for this wave: less than one run
-    for (; k < g.K && k < (g.K + 64 * S - 1) / (64 * S) * (64 * S); k += NW * 64 * S) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int left = g.K - (k + s * 64 + kc);
-            const v4i fw = load_tail(w + k + s * 64, left);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                    fw, load_tail(a[m] + k + s * 64, left), acc[m], 0, 0, 0);
-        }
-    }
-    join_waves<T, MT, NW>(g, acc, &part[0][0][0], n0, t0, beside);
 }
 
 // ---------------------------------------------------------------------------
@@ -327,6 +334,11 @@ __global__ void __launch_bounds__(64 * NW) gemm_rows_kernel(GemmArgs g)
 // then one barrier: every wave holds all it needs of chunk c, and chunk c + 1
 // has arrived; while the second step is multiplied, chunk c + ST is copied over
 // chunk c and the first operands of chunk c + 1 are read.
+//
+// ANY: operands at any address and any K.  No 16-byte copy into LDS can fetch
+// those, so a chunk goes through registers, and two stages are enough: chunk
+// c + 3 is loaded (at any address) where the copy would be, and chunk c + 2,
+// loaded one chunk before, is stored over chunk c.
 template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Tile8 {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
@@ -360,8 +372,8 @@ struct Tile8 {
         }
     };
 
-    // The tile's sums over the chunks [c0, c1) of K, and whether to write them.
-    template <class T>
+    // The tile's sums over the chunks [c0, c1) of K, written or left for the join.
+    template <class T, bool ANY>
     static __device__ __forceinline__ void run(const GemmArgs &g, int t0, int n0, int c0, int c1,
                                                int tile, int slice, char *lds)
     {
@@ -463,56 +475,122 @@ struct Tile8 {
             }
         };
         Frag f0, f1;
-#pragma unroll
-        for (int i = 0; i < ST; ++i)
-            if (c0 + i < c1)
-                copy_any(c0 + i);
-        // the first chunk has arrived; the ones behind it stay in flight
-        if (c1 - c0 >= ST)
-            wait_copies<(ST - 1) * COPIES>();
-        else
-            wait_copies<0>();
-        __syncthreads();
-        read(f0, 0, 0);
-        int c = c0, stage = 0;
-        const int whole = c1 * KC <= g.K ? c1 : c1 - 1;
-        for (; c + ST < whole; ++c) {
-            const int next = stage + 1 == ST ? 0 : stage + 1;
-            multiply(f0, kReads, [&](int i) { read_one(f1, i, stage, 1); });
-            wait_copies<(ST - 2) * COPIES>();              // chunk c + 1 has arrived
-            __syncthreads();
-            const uint32_t st = lds0 + stage * STAGE;
-            const int8_t *a = abase + (long long)(c + ST) * KC;
-            const int8_t *w = wbase + (long long)(c + ST) * KC;
-            multiply(f1, kReadsAndCopies, [&](int i) {
-                if (i < MT + NT)
-                    read_one(f0, i, next, 0);
-                else
-                    copy16_to_lds(i - MT - NT < ACOPIES ? a : w, off[i - MT - NT],
-                                  st + (i - MT - NT) * NW * 1024);
-            });
-            stage = next;
-        }
         // The scales are on their way while the last chunks are multiplied, where
         // registers are left for them.
         constexpr bool kEarly = NT * MT < 32;
         Scales sc;
-        if (kEarly)
-            sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
-        for (; c < c1; ++c) {                              // the last ones
-            const int next = stage + 1 == ST ? 0 : stage + 1;
-            read(f1, stage, 1);
-            clear_past_k(f0, c * KC);
-            multiply(f0, kNothing, [](int) {});
-            wait_copies<0>();
+        if constexpr (ANY) {
+            v4i held[COPIES];
+            auto at = [&](int i, int c) {
+                return (i < ACOPIES ? abase : wbase) + off[i] + (uint32_t)(c * KC);
+            };
+            auto load = [&](int c) {
+                auto here = [&](int i) { return at(i, c); };
+                auto left = [&](int) { return g.K - c * KC - cplace; };
+                if ((c + 1) * KC <= g.K) {
+#pragma unroll
+                    for (int i = 0; i < COPIES; ++i)
+                        held[i] = load16(here(i));
+                } else if (g.K >= 16) {
+                    load_ends(held, here, left);
+                } else {
+                    load_short(held, here, left);
+                }
+            };
+            auto store_one = [&](int i, int stage) {
+                *reinterpret_cast<v4i *>(lds + stage * STAGE + (i * NW + wave) * 1024 +
+                                         lane * 16) = held[i];
+            };
+            auto store = [&](int stage) {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    store_one(i, stage);
+            };
+#pragma unroll 1
+            for (int i = 0; i < 3 && c0 + i < c1; ++i) {
+                load(c0 + i);
+                if (i < 2)
+                    store(i);
+            }
             __syncthreads();
-            if (c + ST < c1)
-                copy_any(c + ST);                          // part of a chunk
-            if (c + 1 < c1)
-                read(f0, next, 0);
-            clear_past_k(f1, c * KC + 64);
-            multiply(f1, kNothing, [](int) {});
-            stage = next;
+            read(f0, 0, 0);
+            int c = c0, stage = 0;
+            const int whole = c1 * KC <= g.K ? c1 : c1 - 1;
+            for (; c + 3 < whole; ++c, stage ^= 1) {
+                multiply(f0, kReads, [&](int i) { read_one(f1, i, stage, 1); });
+                __syncthreads();
+                multiply(f1, kReadsAndCopies, [&](int i) {
+                    if (i < MT + NT) {
+                        read_one(f0, i, stage ^ 1, 0);
+                    } else {
+                        store_one(i - MT - NT, stage);
+                        held[i - MT - NT] = load16(at(i - MT - NT, c + 3));
+                    }
+                });
+            }
+#pragma unroll 1
+            for (; c < c1; ++c, stage ^= 1) {              // the last ones
+                read(f1, stage, 1);
+                multiply(f0, kNothing, [](int) {});
+                __syncthreads();
+                if (c + 2 < c1)
+                    store(stage);
+                if (c + 3 < c1)
+                    load(c + 3);
+                if (c + 1 < c1)
+                    read(f0, stage ^ 1, 0);
+                multiply(f1, kNothing, [](int) {});
+            }
+            if (kEarly)
+                sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < ST; ++i)
+                if (c0 + i < c1)
+                    copy_any(c0 + i);
+            // the first chunk has arrived; the ones behind it stay in flight
+            if (c1 - c0 >= ST)
+                wait_copies<(ST - 1) * COPIES>();
+            else
+                wait_copies<0>();
+            __syncthreads();
+            read(f0, 0, 0);
+            int c = c0, stage = 0;
+            const int whole = c1 * KC <= g.K ? c1 : c1 - 1;
+            for (; c + ST < whole; ++c) {
+                const int next = stage + 1 == ST ? 0 : stage + 1;
+                multiply(f0, kReads, [&](int i) { read_one(f1, i, stage, 1); });
+                wait_copies<(ST - 2) * COPIES>();          // chunk c + 1 has arrived
+                __syncthreads();
+                const uint32_t st = lds0 + stage * STAGE;
+                const int8_t *a = abase + (long long)(c + ST) * KC;
+                const int8_t *w = wbase + (long long)(c + ST) * KC;
+                multiply(f1, kReadsAndCopies, [&](int i) {
+                    if (i < MT + NT)
+                        read_one(f0, i, next, 0);
+                    else
+                        copy16_to_lds(i - MT - NT < ACOPIES ? a : w, off[i - MT - NT],
+                                      st + (i - MT - NT) * NW * 1024);
+                });
+                stage = next;
+            }
+            if (kEarly)
+                sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
+            for (; c < c1; ++c) {                          // the last ones
+                const int next = stage + 1 == ST ? 0 : stage + 1;
+                read(f1, stage, 1);
+                clear_past_k(f0, c * KC);
+                multiply(f0, kNothing, [](int) {});
+                wait_copies<0>();
+                __syncthreads();
+                if (c + ST < c1)
+                    copy_any(c + ST);                      // part of a chunk
+                if (c + 1 < c1)
+                    read(f0, next, 0);
+                clear_past_k(f1, c * KC + 64);
+                multiply(f1, kNothing, [](int) {});
+                stage = next;
+            }
         }
         if (!kEarly)
             sc.load(g, t0 + wm * (MT * 16) + r, n0 + wn * WCOLS + kq * 4);
@@ -686,7 +764,7 @@ struct Tile8 {
 
 constexpr int kBand = 8;
 
-template <class C, class T>
+template <class C, class T, bool ANY>
 __global__ void __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
 {
@@ -705,7 +783,7 @@ gemm_tile_kernel(GemmArgs g, int tiles_m, int tiles_n)
     const int rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
     const int tm = band * kBand + rest % rows, tn = rest / rows;
     const int chunks = (g.K + C::KC - 1) / C::KC;
-    C::template run<T>(g, tm * C::BM, tn * C::BN, slice * chunks / g.split,
+    C::template run<T, ANY>(g, tm * C::BM, tn * C::BN, slice * chunks / g.split,
                        (slice + 1) * chunks / g.split, id, slice, lds);
 }
 
@@ -720,31 +798,22 @@ hipError_t with_type(int out_dtype, F &&f)
     return f(0.f);
 }
 
-template <class C>
+template <class C, bool ANY>
 hipError_t launch_tile(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     const int tm = (g.T + C::BM - 1) / C::BM, tn = (g.N + C::BN - 1) / C::BN;
     const unsigned grid = (unsigned)((tm * tn * g.split + 7) / 8 * 8);
     return with_type(out_dtype, [&](auto zero) {
-        return launch(gemm_tile_kernel<C, decltype(zero)>, dim3(grid), 64 * C::NW, stream, g, tm, tn);
+        return launch(gemm_tile_kernel<C, decltype(zero), ANY>, dim3(grid), 64 * C::NW, stream, g,
+                      tm, tn);
     });
 }
 
-template <int MT>
-hipError_t launch_rows(const GemmArgs &g, int out_dtype, hipStream_t stream)
-{
-    constexpr int NW = 16;
-    const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.T + MT * 16 - 1) / (MT * 16)));
-    return with_type(out_dtype, [&](auto zero) {
-        return launch(gemm_rows_kernel<decltype(zero), MT, NW>, grid, 64 * NW, stream, g);
-    });
-}
-
-template <int TC, int NW, int R>
+template <int TC, int NW, int R, bool ANY>
 hipError_t launch_stream(const GemmArgs &g, int out_dtype, hipStream_t stream)
 {
     return with_type(out_dtype, [&](auto zero) {
-        return launch(gemm_stream_kernel<decltype(zero), TC, NW, R>,
+        return launch(gemm_stream_kernel<decltype(zero), TC, NW, R, ANY>,
                       dim3((unsigned)((g.N + 15) / 16)), 64 * NW, stream, g);
     });
 }
@@ -826,39 +895,50 @@ GemmPlan gemm_plan(int T, int N, int K)
     return p;
 }
 
+namespace {
+
+template <bool ANY>
+hipError_t launch_planned(const GemmArgs &g, const GemmPlan &p, int out_dtype, hipStream_t stream)
+{
+    if (p.variant == 1) {
+        // through registers, 256 x 256 would need more of them than there are:
+        // two tiles of 128 x 256 (no more workspace than the planned tile)
+        if constexpr (!ANY)
+            if (p.bm == 256)
+                return launch_tile<Tile8<256, 256, 2, 4, 2>, ANY>(g, out_dtype, stream);
+        if (p.bn == 256)
+            return launch_tile<Tile8<128, 256, 2, 4, ANY ? 2 : 3>, ANY>(g, out_dtype, stream);
+        if (p.bn == 192)
+            return launch_tile<Tile8<128, 192, 2, 4, ANY ? 2 : 3>, ANY>(g, out_dtype, stream);
+        if (p.bn == 128)
+            return launch_tile<Tile8<128, 128, 2, 4, ANY ? 2 : 4>, ANY>(g, out_dtype, stream);
+        if (p.bm == 128)
+            return launch_tile<Tile8<128, 64, 2, 2, ANY ? 2 : 3>, ANY>(g, out_dtype, stream);
+        return launch_tile<Tile8<64, 64, 2, 2, ANY ? 2 : 4>, ANY>(g, out_dtype, stream);
+    }
+    // Up to 256 workgroups (one a CU): all of the LDS for one, so that most
+    // of its K is in flight at once (N = 4096, K = 4096, T = 4: 5.9 us, with
+    // half the waves 6.3 us).  More: two a CU, so that one starts while the
+    // other joins (N = 16384: 16.1 us against 18.5 us).
+    const bool one = g.N <= 16 * 256;
+    if (g.T <= 8)
+        return one ? launch_stream<1, 16, 2, ANY>(g, out_dtype, stream)
+                   : launch_stream<1, 8, 3, ANY>(g, out_dtype, stream);
+    if (g.T <= 16)
+        return one ? launch_stream<2, 16, 2, ANY>(g, out_dtype, stream)
+                   : launch_stream<2, 8, 2, ANY>(g, out_dtype, stream);
+    if (g.T <= 32)
+        return launch_stream<4, 4, 3, ANY>(g, out_dtype, stream);
+    return launch_stream<8, 4, 2, ANY>(g, out_dtype, stream);
+}
+
+}  // namespace
+
 hipError_t launch_gemm_w8a8(const GemmArgs &g, const GemmPlan &p, int out_dtype,
                             hipStream_t stream)
 {
-    if (p.variant == 1 && aligned16(g)) {
-        if (p.bm == 256)
-            return launch_tile<Tile8<256, 256, 2, 4, 2>>(g, out_dtype, stream);
-        if (p.bn == 256)
-            return launch_tile<Tile8<128, 256, 2, 4, 3>>(g, out_dtype, stream);
-        if (p.bn == 192)
-            return launch_tile<Tile8<128, 192, 2, 4, 3>>(g, out_dtype, stream);
-        if (p.bn == 128)
-            return launch_tile<Tile8<128, 128, 2, 4, 4>>(g, out_dtype, stream);
-        if (p.bm == 128)
-            return launch_tile<Tile8<128, 64, 2, 2, 3>>(g, out_dtype, stream);
-        return launch_tile<Tile8<64, 64, 2, 2, 4>>(g, out_dtype, stream);
-    }
-    if (p.variant == 0 && aligned16(g)) {
-        // Up to 256 workgroups (one a CU): all of the LDS for one, so that most
-        // of its K is in flight at once (N = 4096, K = 4096, T = 4: 5.9 us, with
-        // half the waves 6.3 us).  More: two a CU, so that one starts while the
-        // other joins (N = 16384: 16.1 us against 18.5 us).
-        const bool one = g.N <= 16 * 256;
-        if (g.T <= 8)
-            return one ? launch_stream<1, 16, 2>(g, out_dtype, stream)
-                       : launch_stream<1, 8, 3>(g, out_dtype, stream);
-        if (g.T <= 16)
-            return one ? launch_stream<2, 16, 2>(g, out_dtype, stream)
-                       : launch_stream<2, 8, 2>(g, out_dtype, stream);
-        if (g.T <= 32)
-            return launch_stream<4, 4, 3>(g, out_dtype, stream);
-        return launch_stream<8, 4, 2>(g, out_dtype, stream);
-    }
-    return g.T <= 16 ? launch_rows<1>(g, out_dtype, stream) : launch_rows<4>(g, out_dtype, stream);
+    return aligned16(g) ? launch_planned<false>(g, p, out_dtype, stream)
+                        : launch_planned<true>(g, p, out_dtype, stream);
 }
 
 }  // namespace wna16
