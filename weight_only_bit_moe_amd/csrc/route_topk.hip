@@ -119,16 +119,21 @@ __device__ __forceinline__ double weight_of(float l, float top)
 
 // Errors of a 32-bit score, in FP32 roundings of 1 + |c|: a sigmoid is off by
 // less than 4, a softmax by up to 8 of its own and 22 of the sum (16 scores a
-// lane, then 6 steps); adding the bias is one more; a key that gives its lowest
-// log2(EPL) bits to the slot is off by EPL.  Two scores may be in another order
-// in 64 bits if they differ by less than both errors, two groups' sums of two
-// scores if they differ by less than four.
+// lane, then 6 steps); adding the bias is one more.  A key that gives its lowest
+// log2(EPL) bits to the slot moves by up to EPL - 1 units in its last place, each
+// of at most two roundings of |c|, and two keys may move towards each other.  Two
+// scores may be in another order in 64 bits if they differ by less than both
+// errors, two groups' sums of two scores if they differ by less than four.
 template <bool SOFTMAX> constexpr float kScoreError = (SOFTMAX ? 31 : 5) * 0x1p-24f;
+template <bool SOFTMAX, int EPL>
+constexpr float kKeyError = kScoreError<SOFTMAX> + 2 * EPL * 0x1p-24f;   // of |c|
 
-__device__ __forceinline__ bool too_near(float a, float b, float tolerance)
+// Of a >= b, where |a| may be the larger: then a - b is larger still, and the
+// unit that kKeyError counts beyond EPL - 1 covers it.
+__device__ __forceinline__ bool too_near(float a, float b, float fixed, float relative)
 {
     // two infinities differ by a NaN: too near as well
-    return !(__builtin_fabsf(a - b) > tolerance * (1.f + __builtin_fabsf(b)));
+    return !(a - b > fixed + relative * __builtin_fabsf(b));
 }
 
 // Takes the experts outside the best groups out of c.  Returns whether two
@@ -408,8 +413,8 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
             key, a.topk, lane, mine,
             [&](uint32_t k, int win) { return win * EPL + (int)(kSlots - (k & kSlots)); },
             [&](uint32_t last, uint32_t k) {
-                return too_near(value_of(last), value_of(k),
-                                2 * (kScoreError<SOFTMAX> + EPL * 0x1p-24f));
+                return too_near(value_of(last), value_of(k), 2 * kScoreError<SOFTMAX>,
+                                2 * kKeyError<SOFTMAX, EPL>);
             });
         if (near) {
             double d[EPL];
