@@ -123,7 +123,7 @@ __device__ __forceinline__ double weight_of(float l, float top)
 // log2(EPL) bits to the slot moves by up to EPL - 1 units in its last place, each
 // of at most two roundings of |c|, and two keys may move towards each other.  Two
 // scores may be in another order in 64 bits if they differ by less than both
-// errors, two groups' sums of two scores if they differ by less than four.
+// errors, two groups' sums of two scores if they differ by less than all four.
 template <bool SOFTMAX> constexpr float kScoreError = (SOFTMAX ? 31 : 5) * 0x1p-24f;
 template <bool SOFTMAX, int EPL>
 constexpr float kKeyError = kScoreError<SOFTMAX> + 2 * EPL * 0x1p-24f;   // of |c|
@@ -146,24 +146,28 @@ __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int
     int close = 0;                                  // groups within the error, itself included
     // a group's two largest; with one expert left (or one in all) that one
     auto total = [&](C one, C two) { return two > kOut ? one + two : one; };
-    auto count = [&](C score, int mine, auto &&of) {
+    auto count = [&](C score, C one, C two, int mine, auto &&of) {
         int ahead = 0;
         if constexpr (sizeof(C) == 4) {
-            // equal scores are near, so 64 bits decide them
-            const float reach = 4 * kScoreError<SOFTMAX> * (1.f + __builtin_fabsf(score));
+            // Equal scores are near, so 64 bits decide them.  The errors are those of the two
+            // scores, which may cancel, and one rounding of their sum.  The group of the two
+            // with the larger error reports the pair.
+            const float reach = 2 * (kScoreError<SOFTMAX> + 0x1p-24f) *
+                                (2.f + __builtin_fabsf(one) + (two > kOut ? __builtin_fabsf(two) : 0.f));
             for (int g = 0; g < a.groups; ++g) {
                 const C o = of(g);
                 ahead += o > score ? 1 : 0;
                 close += __builtin_fabsf(o - score) <= reach ? 1 : 0;
             }
+            // infinite scores, also of two finite ones, go to 64 bits; an empty group does not
+            if (!(score > kOut && score < (C)INFINITY))
+                close = one > kOut ? 2 : 0;
         } else {
             for (int g = 0; g < a.groups; ++g) {
                 const C o = of(g);
                 ahead += o > score || (o == score && g < mine) ? 1 : 0;
             }
         }
-        if (!(score > kOut && score < (C)INFINITY))
-            close = score > kOut ? 2 : 0;           // infinite scores go to 64 bits
         return ahead;
     };
     if (a.span > 0) {
@@ -188,7 +192,7 @@ __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int
             merge(dpp<kMirror>(one), dpp<kMirror>(two));
         const C score = total(one, two);
         const int shift = __ffs(a.span) - 1;
-        const int ahead = count(score, lane >> shift,
+        const int ahead = count(score, one, two, lane >> shift,
                                 [&](int g) { return lane_value(score, g << shift); });
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
@@ -210,7 +214,8 @@ __device__ __forceinline__ bool keep_groups(C (&c)[EPL], const RouteArgs &a, int
             one = v > one ? v : one;
         }
     const C score = total(one, two);
-    const int ahead = count(score, lane, [&](int g) { return lane_value(score, g); });
+    const int ahead =
+        count(score, one, two, lane, [&](int g) { return lane_value(score, g); });
     const uint64_t keep = __ballot(lane < a.groups && ahead < a.topk_groups);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
