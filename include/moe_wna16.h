@@ -421,7 +421,8 @@ int moe_wna16_add_rmsnorm(const void *x, const void *residual, const void *weigh
  * is that of the logits themselves.  An expert whose logit or c is -inf or NaN
  * is never picked; slots without an expert get id -1 and weight 0 (the routed
  * layer skips them).  A logit of +inf counts as the largest finite float.
- * Weights are 0 where p[ids] underflows to 0.
+ * A weight is 0 where p[ids] is 0 in 64 bits: for softmax where the logit is
+ * more than 745.13 below the row's largest, for sigmoid where it is below -709.78.
  *
  *   logits  [T, E] of dtype, rows `stride` apart
  *   bias    [E] float32, or NULL

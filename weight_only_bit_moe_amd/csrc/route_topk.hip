@@ -113,8 +113,14 @@ __device__ __forceinline__ double weight_of(float l, float top)
 {
     if constexpr (SOFTMAX)
         return exp_short((double)l - (double)top);
-    else    // beyond 700 the exponential would overflow; the weight is 0 in FP32 from 104 on
+    else    // from 700 on a constant: below any FP32 number, next to a weight of 2^-100 too
         return reciprocal(1.0 + exp_short(l < -700.f ? 700.0 : -(double)l));
+}
+// Whether exp(l - top) or sigmoid(l) is above 0 in 64 bits.
+template <bool SOFTMAX>
+__device__ __forceinline__ bool has_weight(float l, float top)
+{
+    return SOFTMAX ? (double)l - (double)top > -745.1332191019412 : l > -709.7827f;
 }
 
 // Errors of a 32-bit score, in FP32 roundings of 1 + |c|: a sigmoid is off by
@@ -466,14 +472,22 @@ __global__ void __launch_bounds__(64 * kWaves) route_topk_kernel(RouteArgs a)
             part += l[j] > -INFINITY ? weight_of<SOFTMAX>(l[j], top) : 0.0;
         sum = wave_sum(part);
     }
-    const double p = mine >= 0 ? weight_of<SOFTMAX>(picked, top) : 0.0;
-    if (a.renormalize)
+    double p = mine >= 0 ? weight_of<SOFTMAX>(picked, top) : 0.0;
+    if (a.renormalize) {
         sum = wave_sum(p);
+        if (sum < 0x1p-100) {
+            // Every picked score is tiny, but their ratios need not be: relative to the largest
+            // one.  Both scores are exp(l) there, to 2^-100 (1 + exp(l) is 1).
+            const bool any = mine >= 0 && has_weight<SOFTMAX>(picked, top);
+            const float most = wave_max(any ? picked : -INFINITY);
+            p = any ? exp_short((double)picked - (double)most) : 0.0;
+            sum = wave_sum(p);
+        }
+    }
     if (lane < a.topk) {
         const long long o = (long long)tok * a.topk + lane;
         a.ids[o] = mine;
-        // sums so small that their reciprocal would overflow weigh nothing in FP32 either
-        const double w = sum > 0x1p-1000 ? p * reciprocal(sum) : 0.0;
+        const double w = sum > 0.0 ? p * reciprocal(sum) : 0.0;     // 0: nothing picked has a score
         a.weights[o] = (float)(w * (double)a.scale);
     }
 }
