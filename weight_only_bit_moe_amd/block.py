@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import dataclasses
 import math
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -29,11 +29,62 @@ def channel_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return torch.round(w.float() * inv[:, None]).to(torch.int8), top / 127.0
 
 
+class StepWorkspace(NamedTuple):
+    """Device memory of one step's calls: the routed layer's, and the shared expert's products'."""
+
+    layer: torch.Tensor
+    product: Optional[torch.Tensor]
+
+    def holds(self, layer: int, product: int) -> bool:
+        return (self.layer.numel() >= layer
+                and (not product or (self.product is not None and self.product.numel() >= product)))
+
+
+def _new_workspace(layer: int, product: int, device) -> StepWorkspace:
+    """Of these sizes; the leading bytes that have to start at zero are zeroed on the current stream."""
+    def make(n, sync):
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+        t[:sync].zero_()
+        return t
+    return StepWorkspace(make(max(layer, binding.SYNC_BYTES), binding.SYNC_BYTES),
+                         make(product, block_ops.GEMM_SYNC_BYTES) if product else None)
+
+
+class Workspaces:
+    """Workspaces of steps: one for each stream that steps run on, as large as a step on it has
+    needed so far.  Steps on a stream follow each other there, so the blocks of a model can share
+    one (MoEBlock's workspaces); two host threads that issue steps on one stream need one each.
+
+    A step that is captured into a graph gets memory of the graph's own instead, cleared by the
+    replay: what is kept here is cleared once, when it is made, and a larger one may take its place.
+    """
+
+    def __init__(self):
+        self._kept = {}
+
+    def get(self, layer: int, product: int, device: torch.device) -> StepWorkspace:
+        """A workspace of at least these sizes in bytes, for a step on the device's current stream."""
+        if device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return self.get(layer, product, device)
+        if torch.cuda.is_current_stream_capturing():
+            return _new_workspace(layer, product, device)
+        key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
+        kept = self._kept.get(key)
+        if kept is None or not kept.holds(layer, product):
+            if kept is not None:                    # never smaller than the one it takes the place of
+                layer = max(layer, kept.layer.numel())
+                product = max(product, 0 if kept.product is None else kept.product.numel())
+                del kept, self._kept[key]           # released before the new one is made
+            kept = self._kept[key] = _new_workspace(layer, product, device)
+        return kept
+
+
 @dataclasses.dataclass
 class MoEBlock:
     """Weights and routing of one block.  The routed experts' tensors are forward()'s; the shared
-    expert's are int8 codes with a scale for each channel (channel_codes).  Workspaces are made
-    for a token count on its first use and kept; a block runs one step at a time."""
+    expert's are int8 codes with a scale for each channel (channel_codes).  Steps take their
+    workspace from `workspaces`; pass the same one to all blocks of a model."""
 
     norm: torch.Tensor                      # [H] bf16
     gate: torch.Tensor                      # [E, H] bf16, router
@@ -58,18 +109,27 @@ class MoEBlock:
     beta: float = 0.0
     clamp: Optional[float] = None
     eps: float = 1e-6
-    _kept: dict = dataclasses.field(default_factory=dict, repr=False)
+    workspaces: Workspaces = dataclasses.field(default_factory=Workspaces, repr=False)
+    _need: dict = dataclasses.field(default_factory=dict, repr=False)   # _sizes, kept
 
-    def _workspaces(self, T: int, device):
-        ws = self._kept.get(T)
-        if ws is None:
+    def _sizes(self, T: int):
+        """Bytes that a step's layer and its two products need."""
+        n = self._need.get((T, self.topk))
+        if n is None:
             H, E, I = self.norm.numel(), self.w13.shape[0], self.w13.shape[1] // 2
             two_is, Is = self.shared13.shape[0], self.shared2.shape[1]
-            ws = (binding.workspace_for(T, H, I, E, self.topk, device),
-                  block_ops.gemm_w8a8_workspace_for(T, two_is, H, device),
-                  block_ops.gemm_w8a8_workspace_for(T, H, Is, device))
-            self._kept[T] = ws
-        return ws
+            n = self._need[T, self.topk] = (
+                binding.moe_wna16_workspace_size(T, H, I, E, self.topk),
+                max(block_ops.moe_wna16_gemm_w8a8_workspace_size(T, two_is, H),
+                    block_ops.moe_wna16_gemm_w8a8_workspace_size(T, H, Is)))
+        return n
+
+    def workspace_for(self, T: int) -> StepWorkspace:
+        """A workspace for steps of T tokens that the caller keeps, and clears by making it: for
+        steps captured into a graph, which then need not clear one, one for each graph."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("workspace_for inside a capture: its fill would run in replays only")
+        return _new_workspace(*self._sizes(T), self.norm.device)
 
     def route(self, y: torch.Tensor):
         """Expert ids and routing weights of normed rows y [T, H] bf16."""
@@ -79,23 +139,31 @@ class MoEBlock:
                                     renormalize=self.renormalize, scale=self.route_scale)
 
     def shared(self, q, scale, addend, workspaces=(None, None)):
-        """The shared expert of rows in 8 bits, added to `addend` [T, H] bf16 in place."""
+        """The shared expert of rows in 8 bits, added to `addend` [T, H] bf16 in place.  workspaces:
+        the two products', which may be one."""
         gu = block_ops.gemm_w8a8(q, scale, self.shared13, self.shared13_scale,
                                  workspace=workspaces[0])
         aq, ascale = block_ops.swiglu_quant(gu, alpha=self.alpha, beta=self.beta, clamp=self.clamp)
         return block_ops.gemm_w8a8(aq, ascale, self.shared2, self.shared2_scale, addend=addend,
                                    out=addend, workspace=workspaces[1])
 
-    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                 workspace: Optional[StepWorkspace] = None):
         """x [T, H] bf16, the block's input, and the residual stream it is added to (None at the
-        start of the stack).  Returns (out, residual stream)."""
-        layer_ws, ws13, ws2 = self._workspaces(x.shape[0], x.device)
+        start of the stack).  Returns (out, residual stream).  workspace: from workspace_for, used by
+        one step at a time; one of `workspaces` if not given."""
+        sizes = self._sizes(x.shape[0])
+        if workspace is None:
+            workspace = self.workspaces.get(*sizes, x.device)
+        elif not workspace.holds(*sizes):
+            raise ValueError(f"the workspace is too small for {x.shape[0]} tokens")
         n = block_ops.add_rmsnorm(x, self.norm, residual, eps=self.eps, quant=True)
         ids, w = self.route(n["y"])
         out = binding.forward(n["y"], ids, w, self.w13, self.s13, self.w2, self.s2, bits=self.bits,
                               group=self.group, alpha=self.alpha, beta=self.beta, clamp=self.clamp,
-                              workspace=layer_ws)
-        return self.shared(n["q"], n["scale"], out, (ws13, ws2)), n.get("residual", x)
+                              workspace=workspace.layer)
+        out = self.shared(n["q"], n["scale"], out, (workspace.product, workspace.product))
+        return out, n.get("residual", x)
 
 
 def synthetic(spec, seed: int, device, shared: int = 0) -> MoEBlock:

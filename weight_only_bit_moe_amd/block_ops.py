@@ -29,6 +29,8 @@ except ImportError as e:
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 #: score functions of route_topk (moe_wna16_score)
 SCORES = {"softmax": 0, "sigmoid": 1}
+#: leading bytes of a product's workspace that start at zero (MOE_WNA16_GEMM_SYNC_BYTES)
+GEMM_SYNC_BYTES = 4096
 
 
 def moe_wna16_add_rmsnorm(x, residual, weight, T, H, x_stride, r_stride, dtype, eps, residual_out,
