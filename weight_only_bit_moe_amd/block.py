@@ -87,7 +87,7 @@ class MoEBlock:
     workspace from `workspaces`; pass the same one to all blocks of a model."""
 
     norm: torch.Tensor                      # [H] bf16
-    gate: torch.Tensor                      # [E, H] bf16, router
+    gate: torch.Tensor                      # [E, H], router: float32, or bf16 (rounds the logits too)
     w13: torch.Tensor                       # routed experts: codes and scales
     s13: torch.Tensor
     w2: torch.Tensor
@@ -132,8 +132,8 @@ class MoEBlock:
         return _new_workspace(*self._sizes(T), self.norm.device)
 
     def route(self, y: torch.Tensor):
-        """Expert ids and routing weights of normed rows y [T, H] bf16."""
-        logits = torch.nn.functional.linear(y, self.gate)
+        """Expert ids and routing weights of normed rows y [T, H] bf16, from logits of gate's type."""
+        logits = torch.nn.functional.linear(y.to(self.gate.dtype), self.gate)
         return block_ops.route_topk(logits, self.topk, bias=self.bias, score=self.score,
                                     groups=self.groups, topk_groups=self.topk_groups,
                                     renormalize=self.renormalize, scale=self.route_scale)
