@@ -13,6 +13,7 @@ The raw entry points take integer device addresses, as the others of binding do.
 from __future__ import annotations
 
 import ctypes
+import importlib
 from typing import Optional
 
 import torch
@@ -20,10 +21,13 @@ import torch
 from .binding import OK, MoeWna16Error, load_library
 
 try:
-    from . import _block_ops
-except ImportError as e:
+    _block_ops = importlib.import_module("._block_ops", __package__)
+except ModuleNotFoundError as e:
     raise RuntimeError("the module _block_ops is missing: build it with "
                        "`python -m weight_only_bit_moe_amd.build`") from e
+except ImportError as e:
+    raise RuntimeError(f"the module _block_ops does not load ({e}); if torch has changed since, build "
+                       "it again with `python -m weight_only_bit_moe_amd.build`") from e
 
 #: element types of the operators' 16- and 32-bit tensors (moe_wna16_dtype)
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
