@@ -1,5 +1,5 @@
 """Build the gfx950 shared library libmoe_wna16.so in-tree with hipcc, and the
-Python module _block_ops with g++.
+Python module _block_ops with g++ (or hipcc's clang++) where torch is installed.
 
     python -m weight_only_bit_moe_amd.build
 """
@@ -26,6 +26,11 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found")
+
+
+def llvm_bin() -> str:
+    """The directory of hipcc's own compilers."""
+    return os.path.join(os.path.dirname(os.path.realpath(hipcc())), "..", "llvm", "bin")
 
 
 def flags() -> list:
@@ -59,7 +64,12 @@ def build(verbose: bool = False, jobs: int = 3) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    build_module(verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError as e:
+        print(f"the Python module _block_ops is not built: no torch ({e})", file=sys.stderr)
+    else:
+        build_module(verbose)
     return LIB
 
 
@@ -70,7 +80,7 @@ def build_module(verbose: bool = False) -> str:
     import torch
     at = os.path.dirname(torch.__file__)
     tmp = MODULE + f".tmp{os.getpid()}"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [shutil.which("g++") or os.path.join(llvm_bin(), "clang++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", "/opt/rocm/include", "-isystem", os.path.join(at, "include"),
@@ -95,8 +105,7 @@ SAN_EXE = os.path.join(ROOT, "tests", "sanitize", "host_check")
 
 def build_sanitized(verbose: bool = False) -> str:
     """Build tests/sanitize/host_check; returns its path."""
-    llvm = os.path.join(os.path.dirname(os.path.realpath(hipcc())), "..", "llvm", "bin")
-    clang = os.path.join(llvm, "clang")
+    clang = os.path.join(llvm_bin(), "clang")
     bdir = os.path.join(PKG, "_build")
     os.makedirs(bdir, exist_ok=True)
     objs = []
