@@ -23,10 +23,17 @@ from . import binding, block_ops
 
 def channel_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows of a weight in 8 bits: codes int8 and a float32 scale for each row (channel), the
-    largest magnitude of a row at 127.  Done once, when weights are loaded."""
-    top = w.float().abs().amax(-1)
-    inv = torch.where(top > 0, 127.0 / top, torch.zeros_like(top))
-    return torch.round(w.float() * inv[:, None]).to(torch.int8), top / 127.0
+    largest magnitude of a row at 127.  As in the operators, a row whose largest magnitude is below
+    2^-100 gets zero codes and scale 0, one with a NaN or infinity zero codes and scale NaN.  Done
+    once, when weights are loaded."""
+    v = w.float()
+    top = v.abs().amax(-1)
+    finite = torch.isfinite(top)
+    live = finite & (top >= 2.0 ** -100)
+    mult = torch.where(live, 127.0 / top, torch.zeros_like(top))[:, None]
+    codes = torch.where(live[:, None], torch.round(v * mult), torch.zeros_like(mult)).to(torch.int8)
+    scale = torch.where(live, top / 127.0, torch.zeros_like(top))
+    return codes, torch.where(finite, scale, torch.full_like(top, math.nan))
 
 
 class StepWorkspace(NamedTuple):
