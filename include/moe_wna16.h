@@ -400,7 +400,9 @@ typedef enum {
  * At least one of y_out and q_out.  Tensors aligned to their element size.
  * 0 <= T <= 2^21 (T = 0: no launch), 1 <= H <= 32768, strides >= H, eps >= 0 finite.
  * A row with a NaN or infinity in v gets zero codes and a NaN scale; a row
- * with m < 2^-100 gets zero codes and scale 0.
+ * with m < 2^-100 gets zero codes and scale 0.  Where the sum of squares
+ * overflows FP32 (a root mean square of 1.8e19 / sqrt(H) and more) rstd is 0,
+ * and so are y and the scale; where it is 0 and eps is 0, y is not finite.
  */
 int moe_wna16_add_rmsnorm(const void *x, const void *residual, const void *weight, int T, int H,
                           int64_t x_stride, int64_t r_stride, int dtype, float eps,

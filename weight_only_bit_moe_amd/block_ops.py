@@ -9,6 +9,9 @@ Each runs in the library's gfx950 kernels on the current stream.  Argument
 checks, allocation and the library call are in the compiled module _block_ops
 (csrc/block_ops_module.cpp): decode steps call these every few microseconds.
 The raw entry points take integer device addresses, as the others of binding do.
+
+Inference only, as the rest of the package: tensors that require a gradient are
+taken as values, and no output carries a graph.
 """
 from __future__ import annotations
 

@@ -485,7 +485,7 @@ type), "y" (h * weight / rms(h), if normed) and, with quant, "q" int8 [T, H] and
 "scale" float32 [T] with y about q * scale.  x, residual: bf16, fp16 or fp32, rows
 may be strided; weight [H] of the same type.  Outputs are contiguous (q may have
 strided rows); pass them in to reuse memory (residual_out may be x or residual
-itself).)";
+itself).  No gradient: outputs carry no graph.)";
 
 const char k_route_topk[] = R"(route_topk(logits, topk, *, bias=None, score="softmax", groups=1, topk_groups=1, renormalize=True, scale=1.0, ids=None, weights=None) -> (ids, weights)
 
@@ -495,23 +495,25 @@ reads them, of router logits [T, E] (bf16, fp16 or fp32; rows may be strided).
 score "softmax" or "sigmoid"; bias [E] float32 is added for picking only; with
 groups > 1 only the experts of the topk_groups best groups (by the sum of their
 two largest) are picked.  Experts with a logit of -inf or NaN are never picked;
-slots without an expert get id -1 and weight 0.)";
+slots without an expert get id -1 and weight 0.  No gradient: outputs carry no
+graph.)";
 
 const char k_gemm_w8a8[] = R"(gemm_w8a8(a, a_scale, w, w_scale, *, addend=None, out_dtype=torch.bfloat16, out=None, workspace=None) -> out
 
-(a @ w.T) * a_scale[:, None] * w_scale + addend, the sum exact in int32, rounded
-once.
+(a @ w.T) * a_scale[:, None] * w_scale + addend, the sum exact in int32, the rest in
+FP32, rounded to out_dtype at the end.
 
 a int8 [T, K], a_scale float32 [T]; w int8 [N, K], w_scale float32 [N]; addend
 [T, N] of out_dtype (bf16, fp16, fp32).  Rows may be strided.  out may be the
 addend.  workspace: from gemm_w8a8_workspace_for, kept by the caller and used by
-one call at a time; allocated here when it is needed and not given.)";
+one call at a time; allocated here when it is needed and not given.  No gradient:
+the output carries no graph.)";
 
 const char k_swiglu_quant[] = R"(swiglu_quant(gu, *, alpha=1.0, beta=0.0, clamp=None, q=None, scale=None) -> (q, scale)
 
 SwiGLU of rows gu = [gate (I), up (I)] [T, 2I] (bf16, fp16 or fp32; rows may be
 strided) in 8 bits: codes int8 [T, I] and scale float32 [T].  alpha, beta, clamp
-as in forward().)";
+as in forward().  No gradient: outputs carry no graph.)";
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<f>))
 PyMethodDef methods[] = {
