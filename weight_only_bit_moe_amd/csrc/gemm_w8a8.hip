@@ -3,17 +3,21 @@
 // The sum is exact in int32 (K <= 131071), whatever the order, so splitting K
 // over waves or workgroups changes no result.
 //
+// Times in this file are those of calls one after another in a captured graph,
+// bf16 out, codes distributed as activations' unless it says otherwise; a kernel
+// trace gives 0.5 to 1 us less for the short ones.
+//
 // Up to 64 tokens the weights are streamed once through kernels that are bound
-// by the launch, one memory round trip and HBM (T = 4, N = K = 4096: 5.1 us,
-// 16.8 MB; T = 64, K = 2048: 5.3 us; N = 16384, T = 4: 16 us = 4.2 TB/s).  More
-// tokens go through MFMA tiles (T = 8192, N = K = 4096: 108-124 us = 2.2-2.5
-// POP/s with codes as activations have them, 129-139 us with uniform ones).  In
-// a long run of the tile loop (K = 32768) the MFMAs are busy 72 % of the cycles,
-// at a clock that has fallen to 1.5 GHz: power bounds it, the more bits of the
-// operands change the more.  A library product of the same size takes 128 us.
+// by the launch, one memory round trip and HBM (T = 4, N = K = 4096: 5.5 us,
+// 16.8 MB; T = 64, K = 2048: 5.9 us; N = 16384, T = 4: 14.8 us = 4.5 TB/s).  More
+// tokens go through MFMA tiles (T = 8192, N = K = 4096: 118-126 us = 2.2-2.3
+// POP/s, 131 us with uniform codes).  In a long run of the tile loop (K = 32768,
+// 2.4 POP/s) the MFMAs are busy 72 % of the cycles, at a clock that has fallen to
+// 1.5 GHz: power bounds it, the more bits of the operands change the more.  A
+// library product of the same size takes 128 us.
 // Operands whose rows do not all begin at multiples of 16 bytes go the same ways
-// through registers (N = 4096, K = 4090 against 4096: T = 4 6.2 and 5.6 us, T = 64
-// 11.4 and 8.5 us, T = 256 16.9 and 10.6 us, T = 8192 216 and 127 us): every such
+// through registers (N = 4096, K = 4090 against 4096: T = 4 6.2 and 5.5 us, T = 64
+// 11.4 and 8.5 us, T = 256 16.9 and 10.5 us, T = 8192 215 and 126 us): every such
 // load touches two lines, and an LDS store follows it.
 #include <hip/hip_runtime.h>
 
@@ -832,9 +836,15 @@ namespace {
 // copies and epilogue once; a chunk of 128 K with one workgroup a CU, when few
 // CUs run one and when all do; a chunk for each of two workgroups a CU, where
 // their LDS allows it; every further tile of a CU.  Fitted to N and T that fill
-// the 256 CUs in part, once, twice and four times, at K from 2048 to 16384.
+// the 256 CUs in part, once, twice and four times, at K from 2048 to 16384, with
+// uniform codes: with those of activations most take less, up to a fifth (T = 2047,
+// N = 2056, K = 4096: 25.2 us by the model, 21.8 to 22.7 measured).
 // Large tiles do a chunk's products in less time (2.5 POP/s, where the clock
-// falls for power; 64 x 64: 1.4), small ones cover few rows with more CUs.
+// falls for power; 64 x 64: 1.4), small ones cover few rows with more CUs.  128 x
+// 192 serves sizes that 128 x 256 or 256 x 256 would leave in part idle; without
+// it (K = 4096): T = 1280, N = 4096 24.8 -> 26.8 us; 2047, 2056 22.7 -> 25.9; 3000,
+// 1536 23.7 -> 26.1; 3000, 3000 45.0 -> 53.8; 2048, 6144 58 -> 66; 3000, 6144 81 ->
+// 103; and at K = 1024 768, 6144 11.5 -> 15.8; 1536, 3000 11.2 -> 16.4.
 struct TileCost {
     int bm, bn;
     float once, few, all, two, more;
@@ -848,7 +858,7 @@ constexpr int kMaxSplit = 16;
 
 // With K split over `split` workgroups a tile, the chunks are fewer, every
 // workgroup writes its sums and the last one of a tile reads the others'.
-// N = 512, T = 128, K = 16384 (64 x 64 tiles): 25.7 us whole, 12.4 us in eight;
+// N = 512, T = 128, K = 16384 (64 x 64 tiles): 25.7 us whole, 12.7 us in eight;
 // K = 4096: 10.1 us whole, 9.0 us in four, 10.6 us in eight.
 float tile_cost(const TileCost &c, long long tiles, int chunks, int split)
 {
@@ -868,6 +878,14 @@ GemmPlan gemm_plan(int T, int N, int K)
 {
     GemmPlan p{};
     p.split = 1;
+    // Streaming against tiles (K split where the cost model splits it), us:
+    //              N = 512, K = 4096  N = K = 4096  N = 16384, K = 4096  N = 512, K = 16384
+    //   T = 4           3.8 / 7.8       5.5 / 9.1        14.6 / 19.2          6.6 / 11.5
+    //   T = 16          4.0 / 7.9       5.6 / 9.2        16.7 / 19.5          8.0 / 11.6
+    //   T = 32          4.9 / 7.9       6.7 / 9.2        21.1 / 19.9         10.6 / 11.7
+    //   T = 64          6.7 / 8.0       8.4 / 9.4        26.6 / 20.6         15.5 / 11.8
+    // Past 32 tokens the tiles are ahead where N or K is long (N = K = 16384, T = 64:
+    // 88.2 / 64.3), and 1 to 3 us behind elsewhere.
     if (T <= 64) {
         p.variant = 0;
         p.bm = (T + 7) / 8 * 8;
@@ -917,9 +935,9 @@ hipError_t launch_planned(const GemmArgs &g, const GemmPlan &p, int out_dtype, h
         return launch_tile<Tile8<64, 64, 2, 2, ANY ? 2 : 4>, ANY>(g, out_dtype, stream);
     }
     // Up to 256 workgroups (one a CU): all of the LDS for one, so that most
-    // of its K is in flight at once (N = 4096, K = 4096, T = 4: 5.9 us, with
-    // half the waves 6.3 us).  More: two a CU, so that one starts while the
-    // other joins (N = 16384: 16.1 us against 18.5 us).
+    // of its K is in flight at once (N = 4096, K = 4096, T = 4: 5.5 us, with
+    // half the waves 5.8 us).  More: two a CU, so that one starts while the
+    // other joins (N = 8192: 7.9 us against 8.7 us, N = 16384: 14.8 against 16.8).
     const bool one = g.N <= 16 * 256;
     if (g.T <= 8)
         return one ? launch_stream<1, 16, 2, ANY>(g, out_dtype, stream)

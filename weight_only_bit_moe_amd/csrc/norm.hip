@@ -4,11 +4,13 @@
 // Both are one pass over memory: a workgroup owns a row, every thread keeps
 // its share of the row in registers between the reduction and the output, so
 // each input is read once and each output written once.  They are bound by
-// HBM for many rows and by the launch and one memory round trip for few:
+// HBM for many rows and by the launch and one memory round trip for few.
+// Kernel durations (in a captured graph, one call after another, 1 to 5 us more):
 //   norm, bf16, H = 4096, residual, 16- and 8-bit outputs:
-//     T = 8192  57 us = 5.3 TB/s;  T = 2048  15.1 us = 5.0 TB/s;  T = 4  3.8 us
-//   SwiGLU, bf16, I = 2048:  T = 8192  19.4 us = 4.3 TB/s;  T = 64  4 us
-// (a copy of 2 GiB runs at 4.8 TB/s).
+//     T = 8192  52 us = 5.8 TB/s;  T = 4  3.2 us
+//   SwiGLU, bf16, I = 2048:  T = 8192  18.1 us = 4.6 TB/s;  T = 64  3.4 us
+// (a copy of 2 GiB runs at 4.8 TB/s; part of these rows comes from the last-level
+// cache).  In a graph, FP32: norm T = 8192 104 us = 5.5 TB/s, SwiGLU 30.1 us = 5.0.
 //
 // 8-bit rows.  With v the row before its norm's factor and m = max |v|:
 //   q = rint(v * (127 / m)),  scale = m * rstd / 127.
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(1024) swiglu_quant_kernel(SwigluArgs a)
 
 // Threads and chunks a thread for rows of n elements: one chunk a thread up to
 // 1024 threads.  More waves with less each keep more loads in flight: T = 8192,
-// H = 4096 takes 57 us with one chunk a thread, 63 us with two, 71 us with four.
+// H = 4096 takes 57 us with one chunk a thread, 63 us with two, 71 us with four (in
+// a captured graph).
 template <class F>
 hipError_t with_shape(int n, F &&f)
 {

@@ -16,7 +16,7 @@
 // is that of 64-bit scores: two experts swap only if they agree to about 2^-52.
 // Most tokens need no 64-bit score for it.  The scores are first taken in
 // 32 bits, and the token keeps that order if every comparison that mattered was
-// wider than the two errors (kScoreError below):
+// wider than the errors of both sides (kScoreError and kKeyError below):
 // consecutive picks, the last pick and the first expert left out, and any two
 // groups.  Otherwise the wave repeats the picking in 64 bits.  Without bias and
 // groups the order of c is the order of the logits, which is exact in 32 bits.
@@ -27,8 +27,8 @@
 // that held it moves on to its next.  With few tokens the time is the launch and
 // the chain of memory round trips and reductions (T = 4, E = 256, top-6 of 4 of 8
 // groups: 3.5 us); with many it is the VALU instructions, about 500 a token
-// (T = 8192, top-8: 12 us, of which the VALUs are busy 7; the logits alone take
-// 2 us to read).  Everything in 64 bits took 25 us.
+// (T = 8192, top-8: 11.3 us in a captured graph, of which the VALUs are busy 7; the
+// logits alone take 2 us to read).  Everything in 64 bits took 25 us.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
