@@ -481,6 +481,123 @@ int moe_wna16_swiglu_quant(const void *gu, int T, int I, int64_t gu_stride, int 
                            float beta, float clamp, int8_t *q_out, int64_t q_stride,
                            float *scale_out, hipStream_t stream);
 
+/*
+ * Operators for experts in 8-bit floating point: e4m3 codes (the format without
+ * infinities, largest value 448), a float32 scale for each 128 consecutive
+ * elements of a token and for each 128 x 128 block of a weight.  A part of a
+ * block at the end of a row or a column has a scale of its own; kb below is
+ * ceil(K / 128).
+ */
+
+/*
+ * Rows in e4m3, of x itself or of its SwiGLU (as in moe_wna16_swiglu_quant):
+ *   m     = max |v| over the block's elements (FP32)
+ *   scale = 2^ceil(log2(m / 448)), at least 2^-126
+ *   q     = v / scale rounded to e4m3 (nearest even); the division is exact
+ *
+ *   x         [T, K], rows x_stride apart (SwiGLU: gu [T, 2I], K = I)
+ *   q_out     [T, K] e4m3, rows q_stride apart
+ *   scale_out [T, kb] float32, rows s_stride apart
+ * A block with a NaN or infinity in v gets zero codes and a NaN scale.
+ * 0 <= T <= 2^21 (T = 0: no launch), 1 <= K <= 131072, T * kb <= 2^27, strides >= the
+ * row's length.
+ */
+int moe_wna16_quant_fp8(const void *x, int T, int K, int64_t x_stride, int dtype, void *q_out,
+                        int64_t q_stride, float *scale_out, int64_t s_stride, hipStream_t stream);
+int moe_wna16_swiglu_quant_fp8(const void *gu, int T, int I, int64_t gu_stride, int dtype,
+                               float alpha, float beta, float clamp, void *q_out, int64_t q_stride,
+                               float *scale_out, int64_t s_stride, hipStream_t stream);
+
+/*
+ * Product of such rows with such a weight:
+ *   out[t][n] = sum_b a_scale[t][b] w_scale[n / 128][b] sum_{k in b} a[t][k] w[n][k]
+ *               + addend[t][n]
+ * FP32 sums, rounded once to out_dtype.  The same call gives the same bits.
+ *
+ *   a       [T, K] e4m3, rows lda apart;   a_scale [T, kb] float32, rows lda_s apart
+ *   w       [N, K] e4m3, rows ldw apart;   w_scale [ceil(N / 128), kb], rows ldw_s apart
+ *   addend  [T, N] of out_dtype, rows ld_add apart, or NULL
+ *   out     [T, N] of out_dtype, rows ldo apart; may be the addend itself
+ *           (same rows), must not overlap the inputs otherwise
+ *   workspace  as for moe_wna16_gemm_w8a8: moe_wna16_gemm_fp8_workspace_size bytes,
+ *           its first MOE_WNA16_GEMM_SYNC_BYTES zero before its first use and left so
+ * a and w begin at multiples of 16 bytes, and lda, ldw and K are such multiples
+ * (EALIGN, EUNSUPPORTED for K).  T, N >= 0 up to 2^21 (an empty output: no launch),
+ * 16 <= K <= 131072, strides >= the row's length, those of a, w, addend and out below 2^23.
+ */
+int moe_wna16_gemm_fp8_workspace_size(int T, int N, int K, size_t *bytes_out);
+int moe_wna16_gemm_fp8(const void *a, const float *a_scale, const void *w, const float *w_scale,
+                       const void *addend, int T, int N, int K, int64_t lda, int64_t lda_s,
+                       int64_t ldw, int64_t ldw_s, int64_t ld_add, int64_t ldo, int out_dtype,
+                       void *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same for rows sorted by expert: row i of the output, offsets[e] <= i <
+ * offsets[e + 1], is the product of a's row rows[i] (i without `rows`) with w[e].
+ *
+ *   a        [a_rows, K], a_scale [a_rows, kb]; without `rows` a_rows = R
+ *   w        [E, N, K], rows ldw and experts w_expert apart; w_scale likewise
+ *   offsets  [E + 1] int32 on the GPU, as moe_wna16_sort_tokens gives them:
+ *            not decreasing, from 0, the last at most R (values outside are
+ *            taken as the nearest end; rows of experts in another order are not
+ *            all computed)
+ *   rows     [R] int32 on the GPU, or NULL (a value outside [0, a_rows) is read as 0)
+ *   out      [R, N]; rows from offsets[E] on are not written
+ * Alignment and limits as above, with 0 <= R <= 2^21, 1 <= E <= 1024, w_expert a
+ * multiple of 16, and with `rows` a_rows * lda < 2^32.
+ */
+int moe_wna16_gemm_fp8_grouped(const void *a, const float *a_scale, const void *w,
+                               const float *w_scale, const int32_t *offsets, const int32_t *rows,
+                               int E, int a_rows, int R, int N, int K, int64_t lda, int64_t lda_s,
+                               int64_t ldw, int64_t ldw_s, int64_t w_expert, int64_t ws_expert,
+                               int64_t ldo, int out_dtype, void *out, hipStream_t stream);
+
+/*
+ * Tokens sorted by expert: the pairs p = t * topk + j with ids[p] in [0, E), in
+ * the order of their experts and, for an expert, of p.
+ *   offsets [E + 1]     the sorted pairs before each expert, and their number
+ *   tokens  [T * topk]  the token t of each sorted pair; -1 behind the last
+ *   slots   [T, topk]   the place of each pair; -1 for an id outside [0, E)
+ *   xs      [T * topk, H]  row tokens[i] of x at i; rows behind the last sorted
+ *                       pair are not written
+ *
+ *   ids [T, topk] int32;  x [T, H] of dtype, rows x_stride apart, or NULL (then no xs)
+ *   workspace  moe_wna16_sort_tokens_workspace_size bytes, 4-byte aligned, any contents
+ * 0 <= T <= 2^21 (T = 0 writes nothing but offsets), 1 <= topk <= 64, T * topk <= 2^24,
+ * 1 <= E <= 1024, 1 <= H <= 2^20.
+ */
+int moe_wna16_sort_tokens_workspace_size(int T, int topk, int E, size_t *bytes_out);
+int moe_wna16_sort_tokens(const int32_t *ids, int T, int topk, int E, const void *x, int H,
+                          int64_t x_stride, int dtype, int32_t *tokens_out, int32_t *slots_out,
+                          int32_t *offsets_out, void *xs_out, int64_t xs_stride, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Rows back to their tokens:
+ *   out[t] = sum_j weights[t][j] y[slots[t][j]] + addend[t]
+ * over the slots in [0, R), in FP32 in the order of j, rounded once.  Weights of
+ * one without `weights`.  It is also the gradient of sort_tokens to x.
+ *
+ *   y [R, H] of dtype;  slots [T, topk] int32;  weights [T, topk] float32 or NULL
+ *   addend [T, H] or NULL;  out [T, H], may be the addend itself (same rows)
+ * and the gradients, where no two slots name the same row:
+ *   dy[slots[t][j]] = weights[t][j] dout[t], rounded once
+ *   dw[t][j]        = <dout[t], y[slots[t][j]]> in FP32, 0 for a slot outside [0, R)
+ * dy [R, H] or NULL, dw [T, topk] float32 or NULL (then y may be NULL).  Rows of dy
+ * that no slot names are not written, but with `used` (one int32 on the GPU,
+ * sort_tokens' offsets + E) those from *used on are cleared.
+ * 0 <= T <= 2^21 (0: no launch, for the gradient only without `used`), 0 <= R <= 2^24,
+ * 1 <= topk <= 64, 1 <= H <= 2^20 (gradient: 32768).
+ */
+int moe_wna16_combine_tokens(const void *y, const int32_t *slots, const float *weights,
+                             const void *addend, int T, int topk, int H, int R, int64_t y_stride,
+                             int64_t add_stride, int64_t out_stride, int dtype, void *out,
+                             hipStream_t stream);
+int moe_wna16_combine_tokens_grad(const void *dout, const void *y, const int32_t *slots,
+                                  const float *weights, const int32_t *used, int T, int topk, int H,
+                                  int R, int64_t d_stride, int64_t y_stride, int64_t dy_stride,
+                                  int dtype, void *dy, float *dw, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *moe_wna16_status_string(int status);
 

@@ -24,7 +24,10 @@ EXPORTED = ("moe_wna16_workspace_size", "moe_wna16_workspace_f32_offset",
             "moe_wna16_quantize", "moe_wna16_prepare", "moe_wna16_forward_prepared",
             "moe_wna16_forward_noalloc", "moe_wna16_add_rmsnorm", "moe_wna16_route_topk",
             "moe_wna16_gemm_w8a8_workspace_size", "moe_wna16_gemm_w8a8",
-            "moe_wna16_swiglu_quant", "moe_wna16_status_string")
+            "moe_wna16_swiglu_quant", "moe_wna16_quant_fp8", "moe_wna16_swiglu_quant_fp8",
+            "moe_wna16_gemm_fp8_workspace_size", "moe_wna16_gemm_fp8", "moe_wna16_gemm_fp8_grouped",
+            "moe_wna16_sort_tokens_workspace_size", "moe_wna16_sort_tokens",
+            "moe_wna16_combine_tokens", "moe_wna16_combine_tokens_grad", "moe_wna16_status_string")
 
 
 class QParams(ctypes.Structure):
@@ -98,6 +101,26 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_wna16_gemm_w8a8.restype = i
     lib.moe_wna16_swiglu_quant.argtypes = [P, i, i, i64, i, f, f, f, P, i64, P, P]
     lib.moe_wna16_swiglu_quant.restype = i
+    lib.moe_wna16_quant_fp8.argtypes = [P, i, i, i64, i, P, i64, P, i64, P]
+    lib.moe_wna16_quant_fp8.restype = i
+    lib.moe_wna16_swiglu_quant_fp8.argtypes = [P, i, i, i64, i, f, f, f, P, i64, P, i64, P]
+    lib.moe_wna16_swiglu_quant_fp8.restype = i
+    lib.moe_wna16_gemm_fp8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(sz)]
+    lib.moe_wna16_gemm_fp8_workspace_size.restype = i
+    lib.moe_wna16_gemm_fp8.argtypes = [P, P, P, P, P, i, i, i, i64, i64, i64, i64, i64, i64, i, P, P,
+                                       sz, P]
+    lib.moe_wna16_gemm_fp8.restype = i
+    lib.moe_wna16_gemm_fp8_grouped.argtypes = [P, P, P, P, P, P, i, i, i, i, i, i64, i64, i64, i64, i64,
+                                               i64, i64, i, P, P]
+    lib.moe_wna16_gemm_fp8_grouped.restype = i
+    lib.moe_wna16_sort_tokens_workspace_size.argtypes = [i, i, i, ctypes.POINTER(sz)]
+    lib.moe_wna16_sort_tokens_workspace_size.restype = i
+    lib.moe_wna16_sort_tokens.argtypes = [P, i, i, i, P, i, i64, i, P, P, P, P, i64, P, sz, P]
+    lib.moe_wna16_sort_tokens.restype = i
+    lib.moe_wna16_combine_tokens.argtypes = [P, P, P, P, i, i, i, i, i64, i64, i64, i, P, P]
+    lib.moe_wna16_combine_tokens.restype = i
+    lib.moe_wna16_combine_tokens_grad.argtypes = [P, P, P, P, P, i, i, i, i, i64, i64, i64, i, P, P, P]
+    lib.moe_wna16_combine_tokens_grad.restype = i
     lib.moe_wna16_status_string.argtypes = [i]
     lib.moe_wna16_status_string.restype = ctypes.c_char_p
     _lib = lib

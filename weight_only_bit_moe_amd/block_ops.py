@@ -79,16 +79,21 @@ def moe_wna16_swiglu_quant(gu, T, I, gu_stride, dtype, alpha, beta, clamp, q_out
                                                  q_out, q_stride, scale_out, stream)
 
 
+#: the library's functions that the module calls, in the order of its table
+_FUNCTIONS = ("add_rmsnorm", "route_topk", "gemm_w8a8", "gemm_w8a8_workspace_size", "swiglu_quant",
+              "quant_fp8", "swiglu_quant_fp8", "gemm_fp8", "gemm_fp8_workspace_size",
+              "gemm_fp8_grouped", "sort_tokens", "sort_tokens_workspace_size", "combine_tokens",
+              "combine_tokens_grad")
+
+
 def _load():
     """Loads the library and gives the module its functions; raises if it is not built."""
     lib = load_library()
     _block_ops.bind(_load, MoeWna16Error, tuple(
-        ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.moe_wna16_add_rmsnorm, lib.moe_wna16_route_topk, lib.moe_wna16_gemm_w8a8,
-            lib.moe_wna16_gemm_w8a8_workspace_size, lib.moe_wna16_swiglu_quant)))
+        ctypes.cast(getattr(lib, "moe_wna16_" + f), ctypes.c_void_p).value for f in _FUNCTIONS))
 
 
-_block_ops.bind(_load, MoeWna16Error, (0, 0, 0, 0, 0))
+_block_ops.bind(_load, MoeWna16Error, (0,) * len(_FUNCTIONS))
 add_rmsnorm = _block_ops.add_rmsnorm
 route_topk = _block_ops.route_topk
 gemm_w8a8 = _block_ops.gemm_w8a8

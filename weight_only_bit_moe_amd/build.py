@@ -17,7 +17,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_wna16.so")
 MODULE = os.path.join(PKG, "_block_ops.so")
 SOURCES = ["kernels.hip", "quantize.hip", "prepare.hip", "norm.hip", "route_topk.hip",
-           "gemm_w8a8.hip", "api.hip", "block_api.hip"]
+           "gemm_w8a8.hip", "quant_fp8.hip", "tokens.hip", "gemm_fp8.hip", "api.hip", "block_api.hip",
+           "expert_api.hip"]
+MODULE_SOURCES = ["block_ops_module.cpp", "expert_ops_module.cpp"]
 ARCH = "gfx950"
 
 
@@ -86,7 +88,7 @@ def build_module(verbose: bool = False) -> str:
            "-I", INCLUDE, "-isystem", "/opt/rocm/include", "-isystem", os.path.join(at, "include"),
            "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "block_ops_module.cpp"), "-o", tmp,
+           *(os.path.join(CSRC, s) for s in MODULE_SOURCES), "-o", tmp,
            "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
            "-ltorch_hip", "-lc10", "-lc10_hip"]
     _run(cmd, verbose)
@@ -94,8 +96,8 @@ def build_module(verbose: bool = False) -> str:
     return MODULE
 
 
-# Host-side sanitizer build: the C ABI's host code (api.hip, block_api.hip) and the oracle's C
-# code instrumented with AddressSanitizer and UndefinedBehaviorSanitizer, linked
+# Host-side sanitizer build: the C ABI's host code (api.hip, block_api.hip, expert_api.hip) and the
+# oracle's C code instrumented with AddressSanitizer and UndefinedBehaviorSanitizer, linked
 # with the other library objects into tests/sanitize/host_check (no GPU needed).
 SAN = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=all",
        "-fno-omit-frame-pointer"]
@@ -111,7 +113,7 @@ def build_sanitized(verbose: bool = False) -> str:
     objs = []
     for src in SOURCES:
         obj = os.path.join(bdir, src + ".o")
-        if src in ("api.hip", "block_api.hip"):
+        if src in ("api.hip", "block_api.hip", "expert_api.hip"):
             obj = os.path.join(bdir, src.replace(".hip", ".san.o"))
             # device code as usual; every sanitizer flag applies to the host pass only
             host = [f for flag in SAN for f in ("-Xarch_host", flag)]

@@ -1,0 +1,479 @@
+// Tokens' rows in the order of their experts, and experts' rows back to their
+// tokens, with the gradients.
+//
+// Sort: a stable counting sort of the T * topk (token, expert) pairs.  The slot
+// of a pair is the number of pairs of lower experts, plus the number of earlier
+// pairs of its own expert.  Up to kOneLaunch pairs every workgroup counts all
+// ids itself (a few microseconds from the last-level cache) and places and
+// copies its own tokens: one launch.  More pairs are counted in chunks first,
+// the counts turned into the first slot of each (chunk, expert), and a workgroup
+// then counts only its own chunk.  No order of any atomic matters: they only
+// count.
+//
+// The rows are the bulk: each token's row is read once, into registers, and
+// written to its topk places.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "moe_wna16.h"
+#include "expert_ops.hpp"
+#include "rows.hpp"
+#include "wave.hpp"
+
+namespace wna16 {
+
+namespace {
+
+constexpr int kOneLaunch = 8192;        // pairs
+constexpr int kOwn = 64;                // pairs placed by one workgroup, at least one token's
+constexpr int kChunk = 1024;            // pairs of a counted chunk, about
+constexpr int kThreads = 256;
+constexpr int kMaxExperts = 1024;
+
+struct __attribute__((packed, aligned(2))) Row16 { uint32_t v[4]; };
+
+__device__ __forceinline__ bool valid(int id, int E) { return (unsigned)id < (unsigned)E; }
+
+// Exclusive prefix sums of c[0, n) in LDS, n <= 1024, by a workgroup of 256;
+// returns the total.  Ends with a barrier.
+__device__ __forceinline__ int exclusive_scan(int *c, int n)
+{
+    __shared__ int wave_total[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int v[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = (int)threadIdx.x * 4 + i;
+        v[i] = at < n ? c[at] : 0;
+        sum += v[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d)
+            incl += o;
+    }
+    if (lane == 63)
+        wave_total[wave] = incl;
+    __syncthreads();
+    int before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        before += w < wave ? wave_total[w] : 0;
+        total += wave_total[w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = (int)threadIdx.x * 4 + i;
+        if (at < n)
+            c[at] = before;
+        before += v[i];
+    }
+    __syncthreads();
+    return total;
+}
+
+// Many pairs, first: each chunk's pairs of each expert.
+__global__ void __launch_bounds__(kThreads) count_kernel(SortArgs a)
+{
+    __shared__ int count[kMaxExperts];
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+        count[e] = 0;
+    __syncthreads();
+    const long long first = (long long)blockIdx.x * a.chunk * a.topk, all = (long long)a.T * a.topk;
+    const long long end = first + (long long)a.chunk * a.topk;
+    for (long long p = first + threadIdx.x; p < (end < all ? end : all); p += kThreads) {
+        const int id = a.ids[p];
+        if (valid(id, a.E))
+            atomicAdd(&count[id], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+        a.counts[(size_t)blockIdx.x * a.E + e] = count[e];
+}
+
+// Then: counts of chunks -> first slot of each (chunk, expert), and the offsets.
+// A workgroup of 1024: each expert's chunks in 1024 / span runs.
+__global__ void __launch_bounds__(1024) first_slots_kernel(SortArgs a, int chunks, int span)
+{
+    __shared__ int run[1024], total[kMaxExperts];
+    const int e = (int)threadIdx.x % span, seg = (int)threadIdx.x / span, segs = 1024 / span;
+    const int per = (chunks + segs - 1) / segs;
+    const int c0 = seg * per, c1 = c0 + per < chunks ? c0 + per : chunks;
+    int sum = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c)
+            sum += a.counts[(size_t)c * a.E + e];
+    }
+    run[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < (unsigned)a.E) {
+        int t = 0;
+        for (int s = 0; s < segs; ++s) {
+            const int v = run[s * span + threadIdx.x];
+            run[s * span + threadIdx.x] = t;
+            t += v;
+        }
+        total[threadIdx.x] = t;
+    }
+    __syncthreads();
+    // exclusive scan of the totals by the first wave, 16 experts a lane
+    if (threadIdx.x < 64) {
+        int v[16], s = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int at = (int)threadIdx.x * 16 + i;
+            v[i] = at < a.E ? total[at] : 0;
+            s += v[i];
+        }
+        int incl = s;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(incl, d);
+            if ((int)threadIdx.x >= d)
+                incl += o;
+        }
+        int before = incl - s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int at = (int)threadIdx.x * 16 + i;
+            if (at < a.E) {
+                total[at] = before;
+                a.offsets[at] = before;
+            }
+            before += v[i];
+        }
+        if (threadIdx.x == 63)
+            a.offsets[a.E] = before;
+    }
+    __syncthreads();
+    if (e < a.E) {
+        int slot = total[e] + run[threadIdx.x];
+        for (int c = c0; c < c1; c += 8) {          // eight loads on their way at a time
+            int n[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                n[i] = c + i < c1 ? a.counts[(size_t)(c + i) * a.E + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (c + i < c1)
+                    a.counts[(size_t)(c + i) * a.E + e] = slot;
+                slot += n[i];
+            }
+        }
+    }
+}
+
+// The rest: a workgroup's tokens get their slots, and its part of their columns
+// is copied.  ONE: the only launch, which also writes the offsets.
+template <bool ONE>
+__global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a)
+{
+    __shared__ int base[kMaxExperts], earlier[kMaxExperts], own[kOwn], slot[kOwn];
+    const int t0 = blockIdx.x * a.per_group;
+    const int n_tokens = a.T - t0 < a.per_group ? a.T - t0 : a.per_group;
+    const int P = a.T * a.topk, p0 = t0 * a.topk, n = n_tokens * a.topk;
+    const int chunk = ONE ? 0 : t0 / a.chunk, first = ONE ? 0 : chunk * a.chunk * a.topk;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        base[e] = ONE ? 0 : a.counts[(size_t)chunk * a.E + e];
+        earlier[e] = 0;
+    }
+    if ((int)threadIdx.x < n)
+        own[threadIdx.x] = a.ids[p0 + threadIdx.x];
+    __syncthreads();
+    for (int p = first + (int)threadIdx.x; p < (ONE ? P : p0); p += kThreads) {
+        const int id = a.ids[p];
+        if (!valid(id, a.E))
+            continue;
+        if (ONE)
+            atomicAdd(&base[id], 1);
+        if (!ONE || p < p0)
+            atomicAdd(&earlier[id], 1);
+    }
+    __syncthreads();
+    int total = 0;
+    if constexpr (ONE)
+        total = exclusive_scan(base, a.E);
+    else
+        total = a.offsets[a.E];
+    if ((int)threadIdx.x < n) {
+        const int id = own[threadIdx.x];
+        int s = -1;
+        if (valid(id, a.E)) {
+            s = base[id] + earlier[id];
+            for (int i = 0; i < (int)threadIdx.x; ++i)
+                s += own[i] == id;
+        }
+        slot[threadIdx.x] = s;
+        if (blockIdx.y == 0) {
+            a.slots[p0 + threadIdx.x] = s;
+            if (s >= 0)
+                a.tokens[s] = t0 + (int)threadIdx.x / a.topk;
+        }
+    }
+    __syncthreads();
+    if (blockIdx.y == 0) {
+        if (ONE && blockIdx.x == 0) {
+            for (int e = threadIdx.x; e < a.E; e += kThreads)
+                a.offsets[e] = base[e];
+            if (threadIdx.x == 0)
+                a.offsets[a.E] = total;
+        }
+        // places behind the last sorted pair, this workgroup's share
+        for (int p = total + (int)(blockIdx.x * kThreads + threadIdx.x); p < P;
+             p += (int)gridDim.x * kThreads)
+            a.tokens[p] = -1;
+    }
+    if (!a.x)
+        return;
+    const int chunks = (a.row_bytes + 15) / 16, step = (int)gridDim.y * kThreads;
+    for (int i = 0; i < n_tokens; ++i) {
+        const char *src = a.x + (long long)(t0 + i) * a.x_stride;
+        for (int c = (int)(blockIdx.y * kThreads + threadIdx.x); c < chunks; c += step) {
+            if (c * 16 + 16 <= a.row_bytes) {
+                const Row16 v = *reinterpret_cast<const Row16 *>(src + c * 16);
+                for (int j = 0; j < a.topk; ++j) {
+                    const int s = slot[i * a.topk + j];
+                    if (s >= 0)
+                        *reinterpret_cast<Row16 *>(a.xs + s * a.xs_stride + c * 16) = v;
+                }
+            } else {                                    // the row's end, two bytes at a time
+                for (int b = c * 16; b < a.row_bytes; b += 2) {
+                    const uint16_t v = *reinterpret_cast<const uint16_t *>(src + b);
+                    for (int j = 0; j < a.topk; ++j) {
+                        const int s = slot[i * a.topk + j];
+                        if (s >= 0)
+                            *reinterpret_cast<uint16_t *>(a.xs + s * a.xs_stride + b) = v;
+                    }
+                }
+            }
+        }
+    }
+}
+
+int tokens_a_chunk(int topk, int per_group)
+{
+    const int groups = kChunk / (topk * per_group);
+    return per_group * (groups < 1 ? 1 : groups);
+}
+int tokens_a_group(int T, int topk)
+{
+    const int most = kOwn / topk < 1 ? 1 : kOwn / topk;     // topk <= kOwn
+    const int even = (T + 1023) / 1024;                     // about 1024 workgroups
+    return even < 1 ? 1 : even < most ? even : most;        // T = 0: one, without tokens
+}
+
+}  // namespace
+
+size_t sort_workspace(int T, int topk, int E)
+{
+    if ((long long)T * topk <= kOneLaunch)
+        return 0;
+    const int per = tokens_a_chunk(topk, tokens_a_group(T, topk));
+    return (size_t)((T + per - 1) / per) * E * sizeof(int32_t);
+}
+
+hipError_t launch_sort_tokens(const SortArgs &args, hipStream_t stream)
+{
+    SortArgs a = args;
+    const bool one = (long long)a.T * a.topk <= kOneLaunch;
+    a.per_group = tokens_a_group(a.T, a.topk);
+    a.chunk = tokens_a_chunk(a.topk, a.per_group);
+    const int groups = a.T ? (a.T + a.per_group - 1) / a.per_group : 1;
+    // few tokens: a row's columns over several workgroups
+    int parts = 1;
+    if (a.x)
+        while (parts < 8 && groups * parts < 256 && parts * kThreads * 16 < a.row_bytes)
+            parts *= 2;
+    const dim3 grid((unsigned)groups, (unsigned)parts);
+    if (one)
+        return launch(place_kernel<true>, grid, kThreads, stream, a);
+    const int chunks = (a.T + a.chunk - 1) / a.chunk;
+    hipError_t e = launch(count_kernel, dim3((unsigned)chunks), kThreads, stream, a);
+    if (e != hipSuccess)
+        return e;
+    int span = 64;
+    while (span < a.E)
+        span *= 2;
+    e = launch(first_slots_kernel, dim3(1), 1024, stream, a, chunks, span);
+    if (e != hipSuccess)
+        return e;
+    return launch(place_kernel<false>, grid, kThreads, stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// Combine:  out[t] = sum_j w[t][j] y[slot[t][j]] + add[t], in FP32 in that
+// order, rounded once.  A thread holds 8 columns of one token and has up to kRows
+// rows on their way; the slots and weights are wave-uniform.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kRows = 8;
+
+template <class T>
+__global__ void __launch_bounds__(1024) combine_kernel(CombineArgs a)
+{
+    const int t = blockIdx.x;
+    const int c = (int)(blockIdx.y * a.threads + threadIdx.x) * 8, left = a.H - c;
+    if (left <= 0)
+        return;
+    const int32_t *slots = a.slots + (long long)t * a.topk;
+    const float *weights = a.weights ? a.weights + (long long)t * a.topk : nullptr;
+    const T *y = static_cast<const T *>(a.y) + c;
+    float acc[8] = {};
+    float add[8];
+    if (a.addend)
+        load8(static_cast<const T *>(a.addend) + t * a.add_stride + c, left, add);
+    for (int j0 = 0; j0 < a.topk; j0 += kRows) {
+        float v[kRows][8];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            if (j0 + j < a.topk) {
+                const int s = slots[j0 + j];
+                if ((unsigned)s < (unsigned)a.R)
+                    load8(y + s * a.y_stride, left, v[j]);
+            }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            if (j0 + j < a.topk && (unsigned)slots[j0 + j] < (unsigned)a.R) {
+                const float w = weights ? weights[j0 + j] : 1.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[i] = __builtin_fmaf(w, v[j][i], acc[i]);
+            }
+    }
+    if (a.addend) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[i] += add[i];
+    }
+    store8(static_cast<T *>(a.out) + t * a.out_stride + c, left, acc);
+}
+
+// The gradients:  dy[slot[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[slot[t][j]]>.
+// A workgroup owns a token and holds its row of dout; each row of y is read and
+// each row of dy written once.  Workgroups behind the tokens clear the rows of dy
+// that no token has.
+constexpr int kClearGroups = 256;
+
+template <class T, int R>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
+{
+    __shared__ float part[64][16];
+    const int NT = a.threads;
+    if ((int)blockIdx.x >= a.T) {
+        const int used = *a.used;
+        const float zero[8] = {};
+        for (int s = (used < 0 ? 0 : used) + (int)blockIdx.x - a.T; s < a.R; s += kClearGroups) {
+            T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
+            for (int c = (int)threadIdx.x * 8; c < a.H; c += NT * 8)
+                store8(o + c, a.H - c, zero);
+        }
+        return;
+    }
+    const int t = blockIdx.x;
+    const int32_t *slots = a.slots + (long long)t * a.topk;
+    const T *d = static_cast<const T *>(a.dout) + t * a.d_stride;
+    float g[R][8];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int c = (i * NT + (int)threadIdx.x) * 8;
+        load8(d + c, a.H - c, g[i]);
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j = 0; j < a.topk; ++j) {
+        const int s = slots[j];
+        const bool here = (unsigned)s < (unsigned)a.R;
+        float dot = 0.f;
+        if (here) {
+            if (a.dw) {
+                const T *y = static_cast<const T *>(a.y) + s * a.y_stride;
+                float v[R][8];
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int c = (i * NT + (int)threadIdx.x) * 8;
+                    load8(y + c, a.H - c, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dot = __builtin_fmaf(g[i][k], v[i][k], dot);
+            }
+            if (a.dy) {
+                const float w = a.weights ? a.weights[(long long)t * a.topk + j] : 1.f;
+                T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int c = (i * NT + (int)threadIdx.x) * 8;
+                    float f[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        f[k] = w * g[i][k];
+                    store8(o + c, a.H - c, f);
+                }
+            }
+        }
+        if (a.dw) {
+            dot = wave_sum(dot);
+            if (lane == 0)
+                part[j][wave] = dot;
+        }
+    }
+    if (!a.dw)
+        return;
+    __syncthreads();
+    if ((int)threadIdx.x < a.topk) {
+        float sum = 0.f;
+        for (int w = 0; w < NT >> 6; ++w)
+            sum += part[threadIdx.x][w];
+        a.dw[(long long)t * a.topk + threadIdx.x] = sum;
+    }
+}
+
+template <class F>
+hipError_t with_type(int dtype, F &&f)
+{
+    if (dtype == MOE_WNA16_BF16)
+        return f(Bf16{});
+    if (dtype == MOE_WNA16_FP16)
+        return f(Fp16{});
+    return f(0.f);
+}
+
+}  // namespace
+
+hipError_t launch_combine_tokens(const CombineArgs &args, int dtype, hipStream_t stream)
+{
+    CombineArgs a = args;
+    const int chunks = (a.H + 7) / 8;
+    a.threads = chunks < 256 ? (chunks + 63) / 64 * 64 : 256;
+    const dim3 grid((unsigned)a.T, (unsigned)((chunks + a.threads - 1) / a.threads));
+    return with_type(dtype, [&](auto zero) {
+        return launch(combine_kernel<decltype(zero)>, grid, a.threads, stream, a);
+    });
+}
+
+hipError_t launch_combine_tokens_grad(const CombineGradArgs &args, int dtype, hipStream_t stream)
+{
+    CombineGradArgs a = args;
+    const int chunks = (a.H + 7) / 8;
+    const dim3 grid((unsigned)(a.T + (a.dy && a.used ? kClearGroups : 0)));
+    auto run = [&](int threads, auto r) {
+        a.threads = threads;
+        constexpr int R = decltype(r)::value;
+        return with_type(dtype, [&](auto zero) {
+            return launch(combine_grad_kernel<decltype(zero), R>, grid, threads, stream, a);
+        });
+    };
+    if (chunks <= 1024)
+        return run((chunks + 63) / 64 * 64, std::integral_constant<int, 1>{});
+    if (chunks <= 2048)
+        return run(1024, std::integral_constant<int, 2>{});
+    return run(1024, std::integral_constant<int, 4>{});
+}
+
+}  // namespace wna16
