@@ -48,13 +48,12 @@ __device__ __forceinline__ void copy4_to_lds(const void *p, uint32_t lds_in)
 
 // Which rows and weights a workgroup's tile has.
 struct Where {
-    int row0, count;            // rows of the output
-    int expert;
-    bool any;
+    int expert, row0, count;    // rows of the output
+    int column;                 // tile column, -1: no such tile
 };
 
-// Grouped: the row tile `tile` (in the order of the experts) of bm rows; with
-// total_out the number of them.  Offsets are held inside [0, rows].
+// Grouped: an expert's rows, and how many tiles of bm rows they make.  Offsets are
+// held inside [0, rows of the output].
 __device__ __forceinline__ int tiles_of(const GemmFp8Args &g, int e, int bm, int &row0, int &rows)
 {
     int lo = 0, hi = 0;
@@ -261,10 +260,12 @@ __global__ void __launch_bounds__(64 * NW) gemm_fp8_stream_kernel(GemmFp8Args g)
     stream_tile<T, TC, NW, R>(g, g.w, g.w_scale, blockIdx.x * 16, 0, g.T, lds);
 }
 
-// A wave's search for row tile `tile` of bm rows: experts in order, 64 at a time.
-__device__ __forceinline__ Where find_tile(const GemmFp8Args &g, int tile, int bm)
+// A wave's search for tile `id`, where every expert in turn has its row tiles
+// times `columns` tiles, rows first: 64 experts at a time.
+__device__ __forceinline__ Where find_tile(const GemmFp8Args &g, int id, int bm, int columns)
 {
     const int lane = threadIdx.x & 63;
+    Where r{0, 0, 0, -1};
     int base = 0;
     for (int e0 = 0; e0 < g.experts; e0 += 64) {
         int row0, rows;
@@ -276,30 +277,29 @@ __device__ __forceinline__ Where find_tile(const GemmFp8Args &g, int tile, int b
             if (lane >= d)
                 incl += o;
         }
-        const uint64_t past = __ballot(base + incl > tile);
+        const uint64_t past = __ballot((base + incl) * columns > id);
         if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            const int first = base + __builtin_amdgcn_readlane(incl - n, l);
-            const int at = (tile - first) * bm;
-            Where r;
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+            const int tiles = __builtin_amdgcn_readlane(n, l);
+            const int rest = id - (base + __builtin_amdgcn_readlane(incl, l) - tiles) * columns;
+            const int at = rest % tiles * bm, left = __builtin_amdgcn_readlane(rows, l) - at;
             r.expert = e0 + l;
             r.row0 = __builtin_amdgcn_readlane(row0, l) + at;
-            const int left = __builtin_amdgcn_readlane(rows, l) - at;
             r.count = left < bm ? left : bm;
-            r.any = true;
-            return r;
+            r.column = rest / tiles;
+            break;
         }
         base += __builtin_amdgcn_readlane(incl, 63);
     }
-    return Where{0, 0, 0, false};
+    return r;
 }
 
 template <class T, int TC, int NW, int R>
 __global__ void __launch_bounds__(64 * NW) gemm_fp8_grouped_stream_kernel(GemmFp8Args g)
 {
     __shared__ __attribute__((aligned(1024))) char lds[stream_lds<TC, NW, R>()];
-    const Where at = find_tile(g, blockIdx.y, 8 * TC);
-    if (!at.any)
+    const Where at = find_tile(g, blockIdx.y, 8 * TC, 1);
+    if (at.column < 0)
         return;
     stream_tile<T, TC, NW, R>(g, g.w + at.expert * g.w_expert, g.w_scale + at.expert * g.ws_expert,
                               blockIdx.x * 16, at.row0, at.count, lds);
@@ -336,7 +336,7 @@ struct TileF8 {
     static constexpr int SCOPIES = BM / 16;                 // of 16 tokens each
     static constexpr int SCALES = ST * STAGE, LDS = SCALES + 2 * SBUF;
     static constexpr int REGION = ST * STAGE / NW;          // a wave's, in the epilogue
-    static constexpr int AR = MT < 4 ? MT : 4;              // token operands held
+    static constexpr int AR = MT < 4 ? 2 : 4;      // token operands held
     static constexpr int N = MT * NT, D = NT < 4 ? 2 : 3;   // FMAs D MFMAs behind
     static_assert(N % 4 == 0 && MT % AR == 0, "registers take turns");
 
@@ -397,12 +397,6 @@ struct TileF8 {
                     copy4_to_lds(sa[i] + b, buf + (uint32_t)((i * NW + wave) * 256));
             if (wave == 0 && lane < 4 * (SROWS - BM))
                 copy4_to_lds(sw + b, buf + BM * 16);
-        };
-        // Chunk c to its stage, with the scales where its run of four begins.
-        auto copy_one = [&](int i, int c) {
-            const uint32_t st = lds0 + (c - c0) % ST * STAGE;
-            copy16_to_lds((i < ACOPIES ? abase : wbase) + (long long)c * KC, off[i],
-                          st + i * NW * 1024);
         };
         auto copy_part = [&](int c) {
             // K past the end (K is a multiple of 16): the row's first piece is
@@ -483,7 +477,8 @@ struct TileF8 {
                 } else {
 #pragma unroll
                     for (int k = 0; k < COPIES; ++k)
-                        copy_one(k, c0 + i);
+                        copy16_to_lds((k < ACOPIES ? abase : wbase) + (long long)(c0 + i) * KC,
+                                      off[k], lds0 + i * STAGE + k * NW * 1024);
                 }
             }
         if (c1 - c0 >= ST)
@@ -495,33 +490,44 @@ struct TileF8 {
         for (int n = 0; n < NT; ++n)
             read_b(n, 0);
         read_a(0, 0, 0);
-        if (AR > 1)
-            read_a(1, 0, 0);
+        read_a(1, 0, 0);
         ws = *reinterpret_cast<const float *>(swt);
         if (c0 == part)
             clear_past_k(c0);
-        // Steps 0 .. MT - 2 of a chunk; actions(k) for k in [first, last) between them.
-        auto head = [&](int stage, int sbuf, auto actions) {
+        // Steps 0 .. MT - 2 of a chunk, with act(j) behind product j.
+        auto head = [&](int stage, int sbuf, auto &&act) {
 #pragma unroll
             for (int j = 0; j < N - NT; ++j) {
-                const int m = j / NT;
-                if (j % NT == 0) {
+                const int m = j / NT, n = j % NT;
+                if (n == 0)
                     f[m % AR] = raw[m % AR] * ws;
-                }
-                __builtin_amdgcn_sched_barrier(0);
                 product(j);
                 __builtin_amdgcn_sched_barrier(0);
-                if (j >= D)
-                    add_up(j - D);
-                else
-                    add_up(N - D + j);                  // the chunk before's
-                if (j % NT == NT - 1 || NT == 1) {
-                }
-                if (j % NT == (NT > 1 ? 1 : 0) && m + 2 < MT && AR > 2)
+                add_up(j >= D ? j - D : N - D + j);     // the first ones are the chunk before's
+                if (n == (AR > 2 ? 1 : NT - 1) && m + 2 < MT)
                     read_a(m + 2, stage, sbuf);
-                if (AR == 2 && j % NT == NT - 1 && m + 2 < MT)
-                    read_a(m + 2, stage, sbuf);
-                actions(j);
+                act(j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // The last step, while block c + 1's first operands are read.
+        auto last = [&](int next, int sbuf, auto &&act) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int j = N - NT + n;
+                if (n == 0)
+                    f[(MT - 1) % AR] = raw[(MT - 1) % AR] * ws;
+                product(j);
+                __builtin_amdgcn_sched_barrier(0);
+                add_up(j - D);
+                read_b(n, next);
+                if (n == 0)
+                    read_a(0, next, sbuf);
+                if (n == (AR > 2 ? 1 : NT - 1))
+                    read_a(1, next, sbuf);
+                if (n == NT - 1)
+                    ws = *reinterpret_cast<const float *>(swt + sbuf);
+                act(n);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -529,63 +535,49 @@ struct TileF8 {
             return ((c - c0) & 4 ? SBUF : 0) + ((c - c0) & 3) * 4;
         };
         head(0, 0, [](int) {});
-        int stage = 0;
-        for (int c = c0; c < c1; ++c) {
-            const int next = stage + 1 == ST ? 0 : stage + 1;
+        int stage = 0, c = c0;
+        // One run of instructions without a branch: the compiler moves the FMAs out
+        // of sight of their products otherwise, and runs out of registers.
+        const int whole = part >= 0 && part < c1 ? c1 - 1 : c1;
+        for (; c + ST < whole; ++c) {
+            const int next = stage + 1 == ST ? 0 : stage + 1, cn = c + ST;
             // chunk c + 1 has arrived, and every wave holds the rest of chunk c
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if (c + ST <= c1)
-                wait_copies<(ST - 2) * COPIES>();
-            else
-                wait_copies<0>();
+            wait_copies<(ST - 2) * COPIES>();
             __syncthreads();
-            const int cn = c + ST;                      // to be copied over chunk c
-            const bool copies = cn < c1 && cn != part, more = c + 1 < c1;
-            if (cn < c1) {
-                if (((cn - c0) & 3) == 0)
-                    copy_scales(cn);
-                if (cn == part)
-                    copy_part(cn);
+            if (((cn - c0) & 3) == 0)
+                copy_scales(cn);
+            const uint32_t st = lds0 + stage * STAGE;
+            const uint8_t *an = abase + (long long)cn * KC, *wn_ = wbase + (long long)cn * KC;
+            const int sbuf = scale_of(c + 1);
+            // chunk cn over chunk c, the copies spread over the chunk's products
+            auto spread = [&](int k) {
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    if (i * (N - NT) / COPIES == k)
+                        copy16_to_lds(i < ACOPIES ? an : wn_, off[i], st + i * NW * 1024);
+            };
+            last(next, sbuf, spread);
+            head(next, sbuf, [&](int j) { spread(j + NT); });
+            stage = next;
+        }
+        for (;; ++c) {                                  // the last ones
+            const int next = stage + 1 == ST ? 0 : stage + 1;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_copies<0>();
+            __syncthreads();
+            if (c + ST < c1) {                          // the part of a chunk
+                if (((c + ST - c0) & 3) == 0)
+                    copy_scales(c + ST);
+                copy_part(c + ST);
             }
             const int sbuf = scale_of(c + 1);
-            // the copies are spread over the chunk's products
-            auto spread = [&](int k) {                  // k of N places
-                if (copies) {
-#pragma unroll
-                    for (int i = 0; i < COPIES; ++i)
-                        if (i * (N - NT) / COPIES == k)
-                            copy_one(i, cn);
-                }
-            };
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {              // the last step
-                const int j = N - NT + n;
-                if (n == 0)
-                    f[(MT - 1) % AR] = raw[(MT - 1) % AR] * ws;
-                __builtin_amdgcn_sched_barrier(0);
-                product(j);
-                __builtin_amdgcn_sched_barrier(0);
-                add_up(j - D);
-                if (more) {
-                    read_b(n, next);
-                    if (AR > 2 && n < 2)
-                        read_a(n, next, sbuf);
-                    if (AR == 2 && n == 0)
-                        read_a(0, next, sbuf);
-                    if (n == NT - 1) {
-                        if (AR == 2)
-                            read_a(1, next, sbuf);
-                        ws = *reinterpret_cast<const float *>(swt + sbuf);
-                    }
-                }
-                spread(n);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (!more)
+            last(next, sbuf, [](int) {});               // past the end: values that nobody uses
+            if (c + 1 == c1)
                 break;
             if (c + 1 == part)
                 clear_past_k(c + 1);
-            head(next, sbuf, [&](int j) { spread(j + NT); });
+            head(next, sbuf, [](int) {});
             stage = next;
         }
 #pragma unroll
@@ -800,33 +792,11 @@ gemm_fp8_grouped_tile_kernel(GemmFp8Args g, int tiles_n)
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((int)(blockIdx.x >> 3) >= per || id >= total)
         return;
-    // the expert whose run of tiles holds id, as find_tile's, with all its columns
-    int base = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 64) {
-        int row0, rows;
-        const int n = tiles_of(g, e0 + lane, C::BM, row0, rows);
-        int incl = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if (lane >= d)
-                incl += o;
-        }
-        const uint64_t past = __ballot((base + incl) * tiles_n > id);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1, e = e0 + l;
-            const int tm = __builtin_amdgcn_readlane(n, l);
-            const int rest = id - (base + __builtin_amdgcn_readlane(incl, l) - tm) * tiles_n;
-            const int at = rest % tm * C::BM, left = __builtin_amdgcn_readlane(rows, l) - at;
-            const int chunks = (g.K + C::KC - 1) / C::KC;
-            C::template run<T>(g, g.w + e * g.w_expert, g.w_scale + e * g.ws_expert,
-                               __builtin_amdgcn_readlane(row0, l) + at,
-                               left < C::BM ? left : C::BM, rest / tm * C::BN, 0, chunks, 0, 0,
-                               lds);
-            return;
-        }
-        base += __builtin_amdgcn_readlane(incl, 63);
-    }
+    const Where at = find_tile(g, id, C::BM, tiles_n);
+    if (at.column < 0)
+        return;
+    C::template run<T>(g, g.w + at.expert * g.w_expert, g.w_scale + at.expert * g.ws_expert, at.row0,
+                       at.count, at.column * C::BN, 0, (g.K + C::KC - 1) / C::KC, 0, 0, lds);
 }
 
 // f(a value of the output type).
