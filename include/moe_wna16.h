@@ -523,7 +523,8 @@ int moe_wna16_swiglu_quant_fp8(const void *gu, int T, int I, int64_t gu_stride, 
  *           its first MOE_WNA16_GEMM_SYNC_BYTES zero before its first use and left so
  * a and w begin at multiples of 16 bytes, and lda, ldw and K are such multiples
  * (EALIGN, EUNSUPPORTED for K).  T, N >= 0 up to 2^21 (an empty output: no launch),
- * 16 <= K <= 131072, strides >= the row's length, those of a, w, addend and out below 2^23.
+ * 16 <= K <= 131072, strides >= the row's length, those of a, w, addend and out below
+ * 2^23, of the scales below 2^20.
  */
 int moe_wna16_gemm_fp8_workspace_size(int T, int N, int K, size_t *bytes_out);
 int moe_wna16_gemm_fp8(const void *a, const float *a_scale, const void *w, const float *w_scale,
@@ -544,7 +545,7 @@ int moe_wna16_gemm_fp8(const void *a, const float *a_scale, const void *w, const
  *   rows     [R] int32 on the GPU, or NULL (a value outside [0, a_rows) is read as 0)
  *   out      [R, N]; rows from offsets[E] on are not written
  * Alignment and limits as above, with 0 <= R <= 2^21, 1 <= E <= 1024, w_expert a
- * multiple of 16, and with `rows` a_rows * lda < 2^32.
+ * multiple of 16, and with `rows` a_rows * lda < 2^32, a_rows * lda_s < 2^30.
  */
 int moe_wna16_gemm_fp8_grouped(const void *a, const float *a_scale, const void *w,
                                const float *w_scale, const int32_t *offsets, const int32_t *rows,

@@ -11,6 +11,7 @@
 namespace {
 
 constexpr long long kMaxStride = 1ll << 23;     // products: 256 rows stay within 32-bit offsets
+constexpr long long kMaxScaleStride = 1ll << 20;
 constexpr int kMaxDim = 1 << 21;
 constexpr int kMaxK = 1 << 17;
 constexpr int kMaxPairs = 1 << 24;
@@ -71,7 +72,8 @@ int check_product(int T, int N, int K, int64_t lda, int64_t lda_s, int64_t ldw, 
         lda_s < blocks_of(K) || ldw_s < blocks_of(K) || ldo < N)
         return MOE_WNA16_EINVAL;
     if (T > kMaxDim || N > kMaxDim || K > kMaxK || K % 16 != 0 || lda >= kMaxStride ||
-        ldw >= kMaxStride || ldo >= kMaxStride)
+        ldw >= kMaxStride || ldo >= kMaxStride || lda_s >= kMaxScaleStride ||
+        ldw_s >= kMaxScaleStride)
         return MOE_WNA16_EUNSUPPORTED;
     return MOE_WNA16_OK;
 }
@@ -173,7 +175,7 @@ int moe_wna16_gemm_fp8_grouped(const void *a, const float *a_scale, const void *
                             ws_expert < (blocks_of(N) - 1) * ldw_s + blocks_of(K))))
         return MOE_WNA16_EINVAL;
     if (E > 1024 || w_expert >= kMaxElements / 1024 || ws_expert >= kMaxElements / 4096 ||
-        a_rows > kMaxDim || (rows && a_rows * lda >= 1ll << 32))
+        a_rows > kMaxDim || (rows && (a_rows * lda >= 1ll << 32 || a_rows * lda_s >= 1ll << 30)))
         return MOE_WNA16_EUNSUPPORTED;
     if (R == 0 || N == 0)
         return MOE_WNA16_OK;

@@ -80,9 +80,8 @@ struct GemmFp8Args {
     int experts, a_rows;                        // grouped: a_rows of a that `rows` names
 };
 struct Fp8Plan {
-    int variant;                                // 0: few tokens, weights streamed, 1: tiles
-    int bm, bn;
-    int split;
+    int tile;                                   // -1: few tokens, weights streamed
+    int split;                                  // K slices a tile
     size_t workspace;
 };
 Fp8Plan gemm_fp8_plan(int T, int N, int K);

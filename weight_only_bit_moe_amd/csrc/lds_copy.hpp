@@ -35,7 +35,38 @@ __device__ __forceinline__ void copy16_to_lds(const void *base_in, uint32_t voff
                  "s"(lds)
                  : "memory", "m0");
 }
+
+// The same from a buffer: voff of the lane and soff of the wave are added, and
+// pieces past the buffer's end come as zeros.
+__device__ __forceinline__ void copy16_to_lds(v4i buffer, uint32_t voff, uint32_t soff_in,
+                                              uint32_t lds_in)
+{
+    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_in);
+    const uint32_t soff = (uint32_t)__builtin_amdgcn_readfirstlane((int)soff_in);
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
+                 "s"(buffer), "s"(soff), "s"(lds)
+                 : "memory", "m0");
+}
+// Each active lane l's 4 bytes land at lds + l * 4.
+__device__ __forceinline__ void copy4_to_lds(v4i buffer, uint32_t voff, uint32_t soff_in,
+                                             uint32_t lds_in)
+{
+    const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_in);
+    const uint32_t soff = (uint32_t)__builtin_amdgcn_readfirstlane((int)soff_in);
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff),
+                 "s"(buffer), "s"(soff), "s"(lds)
+                 : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+// Descriptor of `bytes` bytes at a wave-uniform address: raw, 32-bit elements.
+__device__ __forceinline__ v4i buffer_of(const void *p, uint32_t bytes)
+{
+    const uint64_t b = reinterpret_cast<uintptr_t>(p);
+    return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+               __builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xffffu)),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
 
 // Place of a row's 16-byte piece c among the 8 of its 128-byte LDS row: the 16
 // rows that one MFMA operand read touches are spread over all banks.
