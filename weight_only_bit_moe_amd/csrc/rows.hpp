@@ -12,26 +12,45 @@ namespace wna16 {
 namespace {
 
 // 8 consecutive elements with the element's own alignment: rows of odd length
-// start anywhere, and gfx950 loads and stores 16 bytes at any address.
+// start anywhere, and gfx950 loads and stores 16 bytes at any address.  (Shared
+// with those of a row's end, a load of 16 bytes falls into four: combine_tokens, T =
+// 4096, k = 8, H = 4096 took 75 us instead of 64.)
 template <class T> struct __attribute__((packed, aligned(sizeof(T)))) Pack8 { T v[8]; };
 struct __attribute__((packed, aligned(1))) Codes8 { uint32_t lo, hi; };
+
+// Zeros past the row's end.
+template <class T>
+__device__ __forceinline__ Pack8<T> load_pack8(const T *p, int left)
+{
+    Pack8<T> t;
+    if (left >= 8) {
+        t = *reinterpret_cast<const Pack8<T> *>(p);
+    } else {
+        asm("" : "+v"(p));      // another address to the compiler: it would share the loads
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t.v[j] = j < left ? p[j] : T{};
+    }
+    return t;
+}
 
 template <class T>
 __device__ __forceinline__ void load8(const T *p, int left, float (&f)[8])
 {
-    if (left >= 8) {
-        const Pack8<T> t = *reinterpret_cast<const Pack8<T> *>(p);
+    const Pack8<T> t = load_pack8(p, left);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = to_float(t.v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] = j < left ? to_float(p[j]) : 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+        f[j] = to_float(t.v[j]);
 }
 
-template <class T>
+// 16 bytes past the caches' replacement order (NT): for outputs larger than they are.
+typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store_past(void *p, Words4 v)
+{
+    __builtin_nontemporal_store(v, static_cast<Words4 *>(p));
+}
+
+template <bool NT = false, class T>
 __device__ __forceinline__ void store8(T *p, int left, const float (&f)[8])
 {
     if (left >= 8) {
@@ -39,8 +58,16 @@ __device__ __forceinline__ void store8(T *p, int left, const float (&f)[8])
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             t.v[j] = from_float<T>(f[j]);
-        *reinterpret_cast<Pack8<T> *>(p) = t;
+        if constexpr (!NT) {
+            *reinterpret_cast<Pack8<T> *>(p) = t;
+        } else {
+            struct { Words4 w[sizeof(T) / 2]; } u = __builtin_bit_cast(decltype(u), t);
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+                store_past(reinterpret_cast<char *>(p) + 16 * k, u.w[k]);
+        }
     } else {
+        asm("" : "+v"(p));
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < left)

@@ -1,14 +1,13 @@
 // Tokens' rows in the order of their experts, and experts' rows back to their
 // tokens, with the gradients.
 //
-// Sort: a stable counting sort of the T * topk (token, expert) pairs.  The slot
-// of a pair is the number of pairs of lower experts, plus the number of earlier
-// pairs of its own expert.  Up to kOneLaunch pairs every workgroup counts all
-// ids itself (a few microseconds from the last-level cache) and places and
-// copies its own tokens: one launch.  More pairs are counted in chunks first,
-// the counts turned into the first slot of each (chunk, expert), and a workgroup
-// then counts only its own chunk.  No order of any atomic matters: they only
-// count.
+// Sort: the slot of a (token, expert) pair is the number of pairs of lower experts,
+// plus the number of earlier pairs of its own expert.  Up to kOneLaunch pairs
+// every workgroup compares its own tokens' pairs with all ids: one launch, and
+// the tokens' rows are on their way meanwhile.  More pairs are counted in chunks
+// first; a workgroup then needs the counts of all chunks and the ids of its own.
+// Past kManyChunks chunks a launch in between turns the counts into the first
+// slot of each (chunk, expert).  No order of any atomic matters: they only count.
 //
 // The rows are the bulk: each token's row is read once, into registers, and
 // written to its topk places.
@@ -25,13 +24,14 @@ namespace wna16 {
 
 namespace {
 
-constexpr int kOneLaunch = 8192;        // pairs
+constexpr int kOneLaunch = 4096;        // pairs
 constexpr int kOwn = 64;                // pairs placed by one workgroup, at least one token's
 constexpr int kChunk = 1024;            // pairs of a counted chunk, about
+constexpr int kManyChunks = 64;
 constexpr int kThreads = 256;
 constexpr int kMaxExperts = 1024;
 
-struct __attribute__((packed, aligned(2))) Row16 { uint32_t v[4]; };
+typedef uint32_t Row16 __attribute__((ext_vector_type(4), aligned(2)));  // at any element
 
 __device__ __forceinline__ bool valid(int id, int E) { return (unsigned)id < (unsigned)E; }
 
@@ -167,38 +167,168 @@ __global__ void __launch_bounds__(1024) first_slots_kernel(SortArgs a, int chunk
     }
 }
 
-// The rest: a workgroup's tokens get their slots, and its part of their columns
-// is copied.  ONE: the only launch, which also writes the offsets.
-template <bool ONE>
-__global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a)
+template <bool NT>
+__device__ __forceinline__ void put(char *p, Row16 v)
+{
+    if constexpr (NT)
+        store_past(p, Words4{v[0], v[1], v[2], v[3]});
+    else
+        *reinterpret_cast<Row16 *>(p) = v;
+}
+
+// Rows of a workgroup's tokens [t0, t0 + n), this workgroup's part of their columns,
+// to the places slot[] (LDS).
+template <bool NT>
+__device__ __forceinline__ void copy_rows(const SortArgs &a, int t0, int n, const int *slot)
+{
+    const int chunks = a.row_bytes / 16, step = (int)gridDim.y * kThreads;
+    const int c0 = (int)(blockIdx.y * kThreads + threadIdx.x);
+    for (int i = 0; i < n; ++i) {
+        const char *src = a.x + (long long)(t0 + i) * a.x_stride;
+        for (int c = c0; c < chunks; c += 2 * step) {
+            const bool two = c + step < chunks;
+            const Row16 v = *reinterpret_cast<const Row16 *>(src + c * 16);
+            const Row16 w = *reinterpret_cast<const Row16 *>(src + (two ? c + step : c) * 16);
+            for (int j = 0; j < a.topk; ++j) {
+                const int s = __builtin_amdgcn_readfirstlane(slot[i * a.topk + j]);
+                if (s < 0)
+                    continue;
+                char *to = a.xs + s * a.xs_stride;
+                put<NT>(to + c * 16, v);
+                if (two)
+                    put<NT>(to + (c + step) * 16, w);
+            }
+        }
+        // the row's end, two bytes a thread
+        const int b = chunks * 16 + (int)threadIdx.x * 2;
+        if (blockIdx.y == 0 && b < a.row_bytes) {
+            const uint16_t v = *reinterpret_cast<const uint16_t *>(src + b);
+            for (int j = 0; j < a.topk; ++j) {
+                const int s = slot[i * a.topk + j];
+                if (s >= 0)
+                    *reinterpret_cast<uint16_t *>(a.xs + s * a.xs_stride + b) = v;
+            }
+        }
+    }
+}
+
+// One launch: up to 256 * PER pairs.  The workgroups behind the tokens' (one a part)
+// write the offsets and mark the places behind the last pair.
+template <int PER>
+__global__ void __launch_bounds__(kThreads) sort_one_kernel(SortArgs a)
+{
+    __shared__ int own[kOwn], slot[kOwn], count[kMaxExperts];
+    const int P = a.T * a.topk;
+    int id[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int p = i * kThreads + (int)threadIdx.x;
+        id[i] = p < P ? a.ids[p] : -1;
+        id[i] = valid(id[i], a.E) ? id[i] : INT32_MAX;      // after all experts
+    }
+    const int t0 = blockIdx.x * a.per_group;
+    if (t0 >= a.T) {                                        // the last workgroup of the row
+        if (blockIdx.y != 0)
+            return;
+        for (int e = threadIdx.x; e < a.E; e += kThreads)
+            count[e] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (id[i] != INT32_MAX)
+                atomicAdd(&count[id[i]], 1);
+        __syncthreads();
+        const int total = exclusive_scan(count, a.E);
+        for (int e = threadIdx.x; e < a.E; e += kThreads)
+            a.offsets[e] = count[e];
+        if (threadIdx.x == 0)
+            a.offsets[a.E] = total;
+        for (int p = total + (int)threadIdx.x; p < P; p += kThreads)
+            a.tokens[p] = -1;
+        return;
+    }
+    const int n_tokens = a.T - t0 < a.per_group ? a.T - t0 : a.per_group;
+    const int p0 = t0 * a.topk, n = n_tokens * a.topk;
+    if ((int)threadIdx.x < n) {
+        const int e = a.ids[p0 + threadIdx.x];
+        own[threadIdx.x] = valid(e, a.E) ? e : -1;
+        slot[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    for (int j = 0; j < n; ++j) {
+        const int e = __builtin_amdgcn_readfirstlane(own[j]);
+        if (e < 0)
+            continue;
+        int before = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool earlier = i * kThreads + (int)threadIdx.x < p0 + j;
+            before += (int)__popcll(__ballot(id[i] < e + (earlier ? 1 : 0)));
+        }
+        if ((threadIdx.x & 63) == 0)
+            atomicAdd(&slot[j], before);
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < n) {
+        const int s = own[threadIdx.x] < 0 ? -1 : slot[threadIdx.x];
+        slot[threadIdx.x] = s;                              // its own entry only
+        if (blockIdx.y == 0) {
+            a.slots[p0 + threadIdx.x] = s;
+            if (s >= 0)
+                a.tokens[s] = t0 + (int)threadIdx.x / a.topk;
+        }
+    }
+    if (!a.x)
+        return;
+    __syncthreads();
+    copy_rows<false>(a, t0, n_tokens, slot);
+}
+
+// Many pairs: a workgroup's tokens get their slots, and its part of their columns is
+// copied.  FIRST: the counts have been turned into first slots and offsets.
+template <bool FIRST, bool NT>
+__global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a, int chunks)
 {
     __shared__ int base[kMaxExperts], earlier[kMaxExperts], own[kOwn], slot[kOwn];
     const int t0 = blockIdx.x * a.per_group;
     const int n_tokens = a.T - t0 < a.per_group ? a.T - t0 : a.per_group;
     const int P = a.T * a.topk, p0 = t0 * a.topk, n = n_tokens * a.topk;
-    const int chunk = ONE ? 0 : t0 / a.chunk, first = ONE ? 0 : chunk * a.chunk * a.topk;
+    const int chunk = t0 / a.chunk, first = chunk * a.chunk * a.topk;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        base[e] = ONE ? 0 : a.counts[(size_t)chunk * a.E + e];
-        earlier[e] = 0;
+        if constexpr (FIRST) {
+            base[e] = a.counts[(size_t)chunk * a.E + e];
+            earlier[e] = 0;
+        } else {
+            int all = 0, mine = 0;
+            for (int c = 0; c < chunks; c += 8) {           // eight loads on their way at a time
+                int v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = c + i < chunks ? a.counts[(size_t)(c + i) * a.E + e] : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    all += v[i];
+                    mine += c + i < chunk ? v[i] : 0;
+                }
+            }
+            base[e] = all;
+            earlier[e] = mine;
+        }
     }
     if ((int)threadIdx.x < n)
         own[threadIdx.x] = a.ids[p0 + threadIdx.x];
     __syncthreads();
-    for (int p = first + (int)threadIdx.x; p < (ONE ? P : p0); p += kThreads) {
+    for (int p = first + (int)threadIdx.x; p < p0; p += kThreads) {
         const int id = a.ids[p];
-        if (!valid(id, a.E))
-            continue;
-        if (ONE)
-            atomicAdd(&base[id], 1);
-        if (!ONE || p < p0)
+        if (valid(id, a.E))
             atomicAdd(&earlier[id], 1);
     }
     __syncthreads();
     int total = 0;
-    if constexpr (ONE)
-        total = exclusive_scan(base, a.E);
-    else
+    if constexpr (FIRST)
         total = a.offsets[a.E];
+    else
+        total = exclusive_scan(base, a.E);
     if ((int)threadIdx.x < n) {
         const int id = own[threadIdx.x];
         int s = -1;
@@ -214,9 +344,8 @@ __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a)
                 a.tokens[s] = t0 + (int)threadIdx.x / a.topk;
         }
     }
-    __syncthreads();
     if (blockIdx.y == 0) {
-        if (ONE && blockIdx.x == 0) {
+        if (!FIRST && blockIdx.x == 0) {
             for (int e = threadIdx.x; e < a.E; e += kThreads)
                 a.offsets[e] = base[e];
             if (threadIdx.x == 0)
@@ -229,30 +358,14 @@ __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a)
     }
     if (!a.x)
         return;
-    const int chunks = (a.row_bytes + 15) / 16, step = (int)gridDim.y * kThreads;
-    for (int i = 0; i < n_tokens; ++i) {
-        const char *src = a.x + (long long)(t0 + i) * a.x_stride;
-        for (int c = (int)(blockIdx.y * kThreads + threadIdx.x); c < chunks; c += step) {
-            if (c * 16 + 16 <= a.row_bytes) {
-                const Row16 v = *reinterpret_cast<const Row16 *>(src + c * 16);
-                for (int j = 0; j < a.topk; ++j) {
-                    const int s = slot[i * a.topk + j];
-                    if (s >= 0)
-                        *reinterpret_cast<Row16 *>(a.xs + s * a.xs_stride + c * 16) = v;
-                }
-            } else {                                    // the row's end, two bytes at a time
-                for (int b = c * 16; b < a.row_bytes; b += 2) {
-                    const uint16_t v = *reinterpret_cast<const uint16_t *>(src + b);
-                    for (int j = 0; j < a.topk; ++j) {
-                        const int s = slot[i * a.topk + j];
-                        if (s >= 0)
-                            *reinterpret_cast<uint16_t *>(a.xs + s * a.xs_stride + b) = v;
-                    }
-                }
-            }
-        }
-    }
+    __syncthreads();
+    copy_rows<NT>(a, t0, n_tokens, slot);
 }
+
+// Rows that the last-level cache (256 MB) would not hold until they are read are
+// written past it: T = 4096, k = 8, H = 4096 (268 MB) 60 us instead of 72; no
+// difference at 67 MB.
+bool past_caches(long long rows, long long row_bytes) { return rows * row_bytes > 128ll << 20; }
 
 int tokens_a_chunk(int topk, int per_group)
 {
@@ -288,30 +401,44 @@ hipError_t launch_sort_tokens(const SortArgs &args, hipStream_t stream)
     if (a.x)
         while (parts < 8 && groups * parts < 256 && parts * kThreads * 16 < a.row_bytes)
             parts *= 2;
+    if (one) {
+        const dim3 grid((unsigned)((a.T ? groups : 0) + 1), (unsigned)parts);
+        const int P = a.T * a.topk;
+        if (P <= 2 * kThreads)
+            return launch(sort_one_kernel<2>, grid, kThreads, stream, a);
+        if (P <= 8 * kThreads)
+            return launch(sort_one_kernel<8>, grid, kThreads, stream, a);
+        return launch(sort_one_kernel<kOneLaunch / kThreads>, grid, kThreads, stream, a);
+    }
     const dim3 grid((unsigned)groups, (unsigned)parts);
-    if (one)
-        return launch(place_kernel<true>, grid, kThreads, stream, a);
     const int chunks = (a.T + a.chunk - 1) / a.chunk;
     hipError_t e = launch(count_kernel, dim3((unsigned)chunks), kThreads, stream, a);
     if (e != hipSuccess)
         return e;
+    const bool nt = a.x && past_caches((long long)a.T * a.topk, a.row_bytes);
+    if (chunks <= kManyChunks)
+        return launch(nt ? place_kernel<false, true> : place_kernel<false, false>, grid, kThreads,
+                      stream, a, chunks);
     int span = 64;
     while (span < a.E)
         span *= 2;
     e = launch(first_slots_kernel, dim3(1), 1024, stream, a, chunks, span);
     if (e != hipSuccess)
         return e;
-    return launch(place_kernel<false>, grid, kThreads, stream, a);
+    return launch(nt ? place_kernel<true, true> : place_kernel<true, false>, grid, kThreads, stream, a,
+                  chunks);
 }
 
 // ---------------------------------------------------------------------------
 // Combine:  out[t] = sum_j w[t][j] y[slot[t][j]] + add[t], in FP32 in that
 // order, rounded once.  A thread holds 8 columns of one token and has up to kRows
-// rows on their way; the slots and weights are wave-uniform.
+// rows on their way; the slots and weights are wave-uniform.  Four rows leave
+// registers for more waves than eight: T = 8192, k = 8, H = 4096 116 us = 5.2 TB/s
+// against 121 us (two thirds of the rows' bytes as T = 680, k = 6: 7.7 against 9.9).
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kRows = 8;
+constexpr int kRows = 4;
 
 template <class T>
 __global__ void __launch_bounds__(1024) combine_kernel(CombineArgs a)
@@ -359,17 +486,17 @@ __global__ void __launch_bounds__(1024) combine_kernel(CombineArgs a)
 // that no token has.
 constexpr int kClearGroups = 256;
 
-template <class T, int R>
+template <class T, int R, bool NT>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
 {
     __shared__ float part[64][16];
-    const int NT = a.threads;
+    const int threads = a.threads;
     if ((int)blockIdx.x >= a.T) {
         const int used = *a.used;
         const float zero[8] = {};
         for (int s = (used < 0 ? 0 : used) + (int)blockIdx.x - a.T; s < a.R; s += kClearGroups) {
             T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
-            for (int c = (int)threadIdx.x * 8; c < a.H; c += NT * 8)
+            for (int c = (int)threadIdx.x * 8; c < a.H; c += threads * 8)
                 store8(o + c, a.H - c, zero);
         }
         return;
@@ -380,47 +507,66 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
     float g[R][8];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int c = (i * NT + (int)threadIdx.x) * 8;
+        const int c = (i * threads + (int)threadIdx.x) * 8;
         load8(d + c, a.H - c, g[i]);
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int j = 0; j < a.topk; ++j) {
-        const int s = slots[j];
-        const bool here = (unsigned)s < (unsigned)a.R;
-        float dot = 0.f;
-        if (here) {
-            if (a.dw) {
-                const T *y = static_cast<const T *>(a.y) + s * a.y_stride;
-                float v[R][8];
+    // lane j holds pair j's slot and weight: read before the first store, behind
+    // which a load would wait for it
+    const int slots_at = lane < a.topk ? slots[lane] : -1;
+    const float weights_at =
+        a.weights && lane < a.topk ? a.weights[(long long)t * a.topk + lane] : 1.f;
+    auto slot = [&](int j) {
+        const int s = __builtin_amdgcn_readlane(slots_at, j);
+        return (unsigned)s < (unsigned)a.R ? s : -1;
+    };
+    // the next row of y is on its way while this one is multiplied
+    Pack8<T> v[R], next[R];
+    auto load = [&](int j, Pack8<T> (&to)[R]) {
+        const int s = j < a.topk ? slot(j) : -1;
+        if (s < 0)
+            return;
+        const T *y = static_cast<const T *>(a.y) + s * a.y_stride;
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int c = (i * NT + (int)threadIdx.x) * 8;
-                    load8(y + c, a.H - c, v[i]);
-                }
+        for (int i = 0; i < R; ++i) {
+            const int c = (i * threads + (int)threadIdx.x) * 8;
+            to[i] = load_pack8(y + c, a.H - c);
+        }
+    };
+    if (a.dw)
+        load(0, v);
+    for (int j = 0; j < a.topk; ++j) {
+        const int s = slot(j);
+        if (a.dw) {
+            load(j + 1, next);
+            float dot = 0.f;
+            if (s >= 0) {
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        dot = __builtin_fmaf(g[i][k], v[i][k], dot);
+                        dot = __builtin_fmaf(g[i][k], to_float(v[i].v[k]), dot);
             }
-            if (a.dy) {
-                const float w = a.weights ? a.weights[(long long)t * a.topk + j] : 1.f;
-                T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int c = (i * NT + (int)threadIdx.x) * 8;
-                    float f[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        f[k] = w * g[i][k];
-                    store8(o + c, a.H - c, f);
-                }
-            }
-        }
-        if (a.dw) {
             dot = wave_sum(dot);
             if (lane == 0)
                 part[j][wave] = dot;
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                v[i] = next[i];
+        }
+        if (a.dy && s >= 0) {
+            const float w =
+                __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weights_at), j));
+            T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = (i * threads + (int)threadIdx.x) * 8;
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    f[k] = w * g[i][k];
+                store8<NT>(o + c, a.H - c, f);
+            }
         }
     }
     if (!a.dw)
@@ -428,7 +574,7 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
     __syncthreads();
     if ((int)threadIdx.x < a.topk) {
         float sum = 0.f;
-        for (int w = 0; w < NT >> 6; ++w)
+        for (int w = 0; w < threads >> 6; ++w)
             sum += part[threadIdx.x][w];
         a.dw[(long long)t * a.topk + threadIdx.x] = sum;
     }
@@ -466,7 +612,11 @@ hipError_t launch_combine_tokens_grad(const CombineGradArgs &args, int dtype, hi
         a.threads = threads;
         constexpr int R = decltype(r)::value;
         return with_type(dtype, [&](auto zero) {
-            return launch(combine_grad_kernel<decltype(zero), R>, grid, threads, stream, a);
+            using T = decltype(zero);
+            return launch(past_caches(a.R, (long long)a.H * sizeof(T))
+                              ? combine_grad_kernel<T, R, true>
+                              : combine_grad_kernel<T, R, false>,
+                          grid, threads, stream, a);
         });
     };
     if (chunks <= 1024)
