@@ -6,9 +6,12 @@
     out     = routed experts of y                                     forward
     out    += shared expert of q: product, SwiGLU in 8 bits, product  gemm_w8a8, swiglu_quant
 
-and returns out and h, the residual stream that the next norm adds out to.
+and returns out and h, the residual stream that the next norm adds out to.  Experts whose weights
+are in 8-bit floating point (block_codes) run in that instead: the routed ones through forward_fp8,
+the shared one through quant_fp8, gemm_fp8 and swiglu_quant_fp8.
 
     python -m weight_only_bit_moe_amd.block --tokens 4      # time of a step on synthetic weights
+    python -m weight_only_bit_moe_amd.block --tokens 4 --fp8
 """
 from __future__ import annotations
 
@@ -18,7 +21,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import binding, block_ops
+from . import binding, block_ops, expert_ops
 
 
 def channel_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -34,6 +37,27 @@ def channel_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     codes = torch.where(live[:, None], torch.round(v * mult), torch.zeros_like(mult)).to(torch.int8)
     scale = torch.where(live, top / 127.0, torch.zeros_like(top))
     return codes, torch.where(finite, scale, torch.full_like(top, math.nan))
+
+
+def block_codes(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Weights [.., N, K] in 8-bit floating point: codes float8_e4m3fn and a float32 scale for each
+    128 x 128 block [.., ceil(N / 128), ceil(K / 128)], the largest magnitude of a block at 448.  A block
+    whose largest magnitude is below 2^-100 gets zero codes and scale 0, one with a NaN or infinity
+    zero codes and scale NaN.  Done once, when weights are loaded that do not come in this form."""
+    N, K = w.shape[-2:]
+    nb, kb = -(-N // 128), -(-K // 128)
+    v = torch.nn.functional.pad(w.float(), (0, kb * 128 - K, 0, nb * 128 - N))
+    v = v.view(*w.shape[:-2], nb, 128, kb, 128)
+    top = v.abs().amax((-3, -1))
+    finite = torch.isfinite(top)
+    live = finite & (top >= 2.0 ** -100)
+    scale = torch.where(live, top / 448.0, torch.zeros_like(top))
+    spread = lambda b: b[..., :, None, :, None]  # noqa: E731
+    # the quotient of a block's largest may round to just above 448, which e4m3 does not hold
+    codes = (v / spread(torch.where(live, scale, torch.ones_like(scale)))).clamp(-448.0, 448.0)
+    codes = torch.where(spread(live), codes, torch.zeros_like(codes))
+    codes = codes.view(*w.shape[:-2], nb * 128, kb * 128)[..., :N, :K].to(torch.float8_e4m3fn)
+    return codes.contiguous(), torch.where(finite, scale, torch.full_like(top, math.nan))
 
 
 class StepWorkspace(NamedTuple):
@@ -89,9 +113,10 @@ class Workspaces:
 
 @dataclasses.dataclass
 class MoEBlock:
-    """Weights and routing of one block.  The routed experts' tensors are forward()'s; the shared
-    expert's are int8 codes with a scale for each channel (channel_codes).  Steps take their
-    workspace from `workspaces`; pass the same one to all blocks of a model."""
+    """Weights and routing of one block.  The routed experts' tensors are forward()'s, or
+    forward_fp8()'s (then bits and group are not used); the shared expert's are int8 codes with a scale
+    for each channel (channel_codes), or e4m3 codes with a scale for each 128 x 128 block (block_codes).
+    Steps take their workspace from `workspaces`; pass the same one to all blocks of a model."""
 
     norm: torch.Tensor                      # [H] bf16
     gate: torch.Tensor                      # [E, H], router: float32, or bf16 (rounds the logits too)
@@ -101,10 +126,10 @@ class MoEBlock:
     s2: torch.Tensor
     bits: Tuple[int, int]
     group: Tuple[int, int]
-    shared13: torch.Tensor                  # [2 Is, H] int8, gate rows then up rows
-    shared13_scale: torch.Tensor            # [2 Is] float32
-    shared2: torch.Tensor                   # [H, Is] int8
-    shared2_scale: torch.Tensor             # [H] float32
+    shared13: torch.Tensor                  # [2 Is, H] int8 or float8, gate rows then up rows
+    shared13_scale: torch.Tensor            # [2 Is] float32, or of blocks
+    shared2: torch.Tensor                   # [H, Is] int8 or float8
+    shared2_scale: torch.Tensor             # [H] float32, or of blocks
     topk: int
     bias: Optional[torch.Tensor] = None     # [E] float32, balance
     score: str = "softmax"
@@ -119,16 +144,26 @@ class MoEBlock:
     workspaces: Workspaces = dataclasses.field(default_factory=Workspaces, repr=False)
     _need: dict = dataclasses.field(default_factory=dict, repr=False)   # _sizes, kept
 
+    @property
+    def routed_fp8(self) -> bool:
+        return self.w13.dtype == torch.float8_e4m3fn
+
+    @property
+    def shared_fp8(self) -> bool:
+        return self.shared13.dtype == torch.float8_e4m3fn
+
     def _sizes(self, T: int):
         """Bytes that a step's layer and its two products need."""
-        n = self._need.get((T, self.topk))
+        key = (T, self.topk, self.routed_fp8, self.shared_fp8)
+        n = self._need.get(key)
         if n is None:
             H, E, I = self.norm.numel(), self.w13.shape[0], self.w13.shape[1] // 2
             two_is, Is = self.shared13.shape[0], self.shared2.shape[1]
-            n = self._need[T, self.topk] = (
-                binding.moe_wna16_workspace_size(T, H, I, E, self.topk),
-                max(block_ops.moe_wna16_gemm_w8a8_workspace_size(T, two_is, H),
-                    block_ops.moe_wna16_gemm_w8a8_workspace_size(T, H, Is)))
+            size = (expert_ops.moe_wna16_gemm_fp8_workspace_size if self.shared_fp8
+                    else block_ops.moe_wna16_gemm_w8a8_workspace_size)
+            n = self._need[key] = (
+                0 if self.routed_fp8 else binding.moe_wna16_workspace_size(T, H, I, E, self.topk),
+                max(size(T, two_is, H), size(T, H, Is)))
         return n
 
     def workspace_for(self, T: int) -> StepWorkspace:
@@ -146,8 +181,14 @@ class MoEBlock:
                                     renormalize=self.renormalize, scale=self.route_scale)
 
     def shared(self, q, scale, addend, workspaces=(None, None)):
-        """The shared expert of rows in 8 bits, added to `addend` [T, H] bf16 in place.  workspaces:
-        the two products', which may be one."""
+        """The shared expert of rows in 8 bits (add_rmsnorm's codes, or quant_fp8's for weights in 8-bit
+        floating point), added to `addend` [T, H] bf16 in place.  workspaces: the two products', which may
+        be one."""
+        if self.shared_fp8:
+            gu = expert_ops.gemm_fp8(q, scale, self.shared13, self.shared13_scale, workspace=workspaces[0])
+            aq, ascale = expert_ops.swiglu_quant_fp8(gu, alpha=self.alpha, beta=self.beta, clamp=self.clamp)
+            return expert_ops.gemm_fp8(aq, ascale, self.shared2, self.shared2_scale, addend=addend,
+                                       out=addend, workspace=workspaces[1])
         gu = block_ops.gemm_w8a8(q, scale, self.shared13, self.shared13_scale,
                                  workspace=workspaces[0])
         aq, ascale = block_ops.swiglu_quant(gu, alpha=self.alpha, beta=self.beta, clamp=self.clamp)
@@ -164,23 +205,49 @@ class MoEBlock:
             workspace = self.workspaces.get(*sizes, x.device)
         elif not workspace.holds(*sizes):
             raise ValueError(f"the workspace is too small for {x.shape[0]} tokens")
-        n = block_ops.add_rmsnorm(x, self.norm, residual, eps=self.eps, quant=True)
+        n = block_ops.add_rmsnorm(x, self.norm, residual, eps=self.eps, quant=not self.shared_fp8)
+        codes = expert_ops.quant_fp8(n["y"]) if self.routed_fp8 or self.shared_fp8 else None
         ids, w = self.route(n["y"])
-        out = binding.forward(n["y"], ids, w, self.w13, self.s13, self.w2, self.s2, bits=self.bits,
-                              group=self.group, alpha=self.alpha, beta=self.beta, clamp=self.clamp,
-                              workspace=workspace.layer)
-        out = self.shared(n["q"], n["scale"], out, (workspace.product, workspace.product))
+        if self.routed_fp8:
+            out = expert_ops.forward_fp8(n["y"], ids, w, self.w13, self.s13, self.w2, self.s2,
+                                         alpha=self.alpha, beta=self.beta, clamp=self.clamp, codes=codes)
+        else:
+            out = binding.forward(n["y"], ids, w, self.w13, self.s13, self.w2, self.s2, bits=self.bits,
+                                  group=self.group, alpha=self.alpha, beta=self.beta, clamp=self.clamp,
+                                  workspace=workspace.layer)
+        q, scale = codes if self.shared_fp8 else (n["q"], n["scale"])
+        out = self.shared(q, scale, out, (workspace.product, workspace.product))
         return out, n.get("residual", x)
 
 
-def synthetic(spec, seed: int, device, shared: int = 0) -> MoEBlock:
+def synthetic(spec, seed: int, device, shared: int = 0, fp8: bool = False) -> MoEBlock:
     """A block with the random routed experts of an inputs.LayerSpec (its T and routing are not
-    used) and random other weights; shared: the shared expert's intermediate size (0: spec.I)."""
+    used) and random other weights; shared: the shared expert's intermediate size (0: spec.I); fp8:
+    all experts' weights random in 8-bit floating point."""
     import numpy as np
 
     from .inputs import make_layer
-    L = make_layer(dataclasses.replace(spec, T=1), seed)
     Is = shared or spec.I
+    if fp8:
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+        randn = lambda *s: torch.randn(*s, generator=g, device=device)  # noqa: E731
+
+        def experts(N, K):      # one after another: all of them in float32 would be large
+            made = [block_codes(randn(N, K) * K ** -0.5) for _ in range(spec.E)]
+            return torch.stack([m[0] for m in made]), torch.stack([m[1] for m in made])
+        w13, s13 = experts(2 * spec.I, spec.H)
+        w2, s2 = experts(spec.H, spec.I)
+        c13, sc13 = block_codes(randn(2 * Is, spec.H) * spec.H ** -0.5)
+        c2, sc2 = block_codes(randn(spec.H, Is) * Is ** -0.5)
+        return MoEBlock(
+            norm=(1 + 0.1 * randn(spec.H)).bfloat16(),
+            gate=(randn(spec.E, spec.H) * spec.H ** -0.5).bfloat16(), w13=w13, s13=s13, w2=w2, s2=s2,
+            bits=(8, 8), group=(128, 128), shared13=c13, shared13_scale=sc13, shared2=c2,
+            shared2_scale=sc2, topk=spec.topk, bias=0.05 * randn(spec.E), score="sigmoid",
+            route_scale=1.0, alpha=spec.alpha, beta=spec.beta,
+            clamp=None if math.isinf(spec.clamp) else spec.clamp)
+    L = make_layer(dataclasses.replace(spec, T=1), seed)
     g = torch.Generator(device=device)
     g.manual_seed(seed)
     randn = lambda *s: torch.randn(*s, generator=g, device=device)  # noqa: E731
@@ -205,9 +272,10 @@ def main() -> None:
                                              "(hidden 4096, 256 experts of 2048, 2-bit codes).")
     ap.add_argument("--tokens", type=int, default=4)
     ap.add_argument("--steps", type=int, default=100)
+    ap.add_argument("--fp8", action="store_true", help="experts in 8-bit floating point instead")
     a = ap.parse_args()
     dev = torch.device("cuda:0")
-    block = synthetic(CONFIGS[2], 1, dev)
+    block = synthetic(CONFIGS[2], 1, dev, fp8=a.fp8)
     H = CONFIGS[2].H
     x, r = (torch.randn(a.tokens, H, device=dev).bfloat16() for _ in range(2))
     for _ in range(5):

@@ -198,19 +198,20 @@ def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch
 def forward_fp8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
                 w13_scale: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor, *,
                 alpha: float = 1.0, beta: float = 0.0, clamp: Optional[float] = None, addend=None,
-                out=None) -> torch.Tensor:
+                out=None, codes=None) -> torch.Tensor:
     """The routed layer with experts in 8-bit floating point: forward() for weights that are e4m3
     codes with a scale for each 128 x 128 block.
 
     x [T, H] (bf16 or fp16); topk_ids int32, topk_w float32 [T, k]; w13 float8_e4m3fn [E, 2I, H],
     gate rows then up rows, w13_scale float32 [E, ceil(2I / 128), ceil(H / 128)]; w2 [E, H, I],
     w2_scale [E, ceil(H / 128), ceil(I / 128)]; H and I multiples of 16.  Ids outside [0, E) are
-    left out.  addend [T, H] is added before the rounding; out may be it.  Returns [T, H] of x's type.
-    Activations are quantized by quant_fp8 and swiglu_quant_fp8; the gate and up rows and the
-    experts' rows are rounded to x's type in between.  No gradient.
+    left out.  addend [T, H] is added before the rounding; out may be it.  codes: quant_fp8(x), where
+    the caller has it.  Returns [T, H] of x's type.  Activations are quantized by quant_fp8 and
+    swiglu_quant_fp8; the gate and up rows and the experts' rows are rounded to x's type in between.
+    No gradient.
 
     Rows of experts that are elsewhere cost memory and a pass of the activation, but no product."""
-    q, scale = quant_fp8(x)
+    q, scale = quant_fp8(x) if codes is None else codes
     s = _block_ops.sort_tokens(topk_ids, w13.shape[0])
     gu = gemm_fp8_grouped(q, scale, w13, w13_scale, s["offsets"], rows=s["tokens"], out_dtype=x.dtype)
     q, scale = swiglu_quant_fp8(gu, alpha=alpha, beta=beta, clamp=clamp)
