@@ -146,7 +146,8 @@ SIZES = [(1, 1, 16), (1, 16, 128), (2, 17, 144), (3, 130, 256), (7, 256, 2048), 
          (16, 64, 4096), (17, 256, 512), (31, 33, 640), (33, 200, 1008), (64, 512, 2048), (65, 70, 112),
          (65, 130, 1024), (100, 257, 272), (128, 512, 4096), (129, 300, 1936), (200, 1025, 528),
          (257, 256, 1152), (300, 640, 4064), (513, 1100, 384), (1000, 264, 2048), (1111, 2049, 400),
-         (2048, 2048, 1024), (3, 8200, 256), (12, 4500, 128), (2500, 2500, 144)]
+         (2048, 2048, 1024), (3, 8200, 256), (12, 4500, 128), (2500, 2500, 144),
+         (1280, 4096, 272), (3000, 1536, 400), (1500, 3000, 528), (4100, 4097, 144), (2047, 2057, 4048)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES)

@@ -306,8 +306,11 @@ struct TileF8 {
     static constexpr int STAGE = (BM + BN) * KC;
     static constexpr int ACOPIES = BM / 8 / NW, COPIES = (BM + BN) / 8 / NW;   // 8 rows each
     static_assert((BM + BN) / 8 % NW == 0 && BM / 8 % NW == 0, "copies divide evenly");
+    static_assert(BN % 64 == 0, "a tile's channels lie in BN / 128 blocks, rounded up");
     static constexpr int WCOLS = BN / WN;
-    static_assert(128 % WCOLS == 0, "a wave's channels lie in one block");
+    // a wave's channels in one block of 128: one scale of the weight; else one for each 16
+    static constexpr bool kOneBlock = 128 % WCOLS == 0;
+    static constexpr int WS = kOneBlock ? 1 : NT;
     // scales: 16 bytes (four blocks) for each token and each 128 channels
     static constexpr int SROWS = BM + (BN + 127) / 128, SBUF = (SROWS * 16 + 63) / 64 * 64;
     static constexpr int SCOPIES = BM / 16;                 // of 16 tokens each
@@ -366,7 +369,7 @@ struct TileF8 {
         // each; one more of wave 0, the weight's.  Blocks past the row's last one are
         // somebody else's or zeros, and not used.
         constexpr int SW = (SCOPIES + NW - 1) / NW;
-        const int kb = (g.K + KC - 1) / KC, wblocks = wlast / 128;
+        const int kb = (g.K + KC - 1) / KC, wblocks = (n0 % 128 + wlast) / 128;
         const v4i asbuf = GATHER ? buffer_of(g.a_scale, (uint32_t)((g.a_rows - 1) * g.lda_s + kb) * 4u)
                                  : buffer_of(g.a_scale + (long long)t0 * g.lda_s,
                                              (uint32_t)((count - 1) * g.lda_s + kb) * 4u);
@@ -412,14 +415,22 @@ struct TileF8 {
         const char *bt[2] = {lds + brow * KC + place(brow, kq) * 16,
                              lds + brow * KC + place(brow, 4 + kq) * 16};
         const char *sat = lds + SCALES + arow * 16;
-        const char *swt = lds + SCALES + (BM + wn * WCOLS / 128) * 16;
+        const char *swt[WS];
+#pragma unroll
+        for (int n = 0; n < WS; ++n)
+            swt[n] = lds + SCALES + (BM + (n0 % 128 + wn * WCOLS + n * 16) / 128) * 16;
         v8i fb[NT], fa[AR];
-        float raw[AR], f[AR], ws = 0.f;
+        float raw[AR], f[4], ws[WS], next_ws[WS];
         v4f tmp[4], acc[NT][MT];
         auto read_b = [&](int n, int stage) {
             const int o = stage * STAGE + n * 16 * KC;
             fb[n] = both(*reinterpret_cast<const v4i *>(bt[0] + o),
                          *reinterpret_cast<const v4i *>(bt[1] + o));
+        };
+        auto read_ws = [&](int sbuf) {
+#pragma unroll
+            for (int n = 0; n < WS; ++n)
+                next_ws[n] = *reinterpret_cast<const float *>(swt[n] + sbuf);
         };
         auto read_a = [&](int m, int stage, int sbuf) {
             const int o = stage * STAGE + m * 16 * KC;
@@ -430,15 +441,19 @@ struct TileF8 {
         // product j's step of 16 tokens and 16 channels
         auto step_of = [](int j) { return 2 * (j / PH) + j % 2; };
         auto channel_of = [](int j) { return j % PH / 2; };
+        // a product's scale: a step's, or its own
+        auto scale_at = [&](int j) { return kOneBlock ? step_of(j) % AR : j % 4; };
         auto add_up = [&](int j) {                      // the FMAs of product j
             const int m = step_of(j), n = channel_of(j);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc[n][m][i] = __builtin_fmaf(tmp[j % 4][i], f[m % AR], acc[n][m][i]);
+                acc[n][m][i] = __builtin_fmaf(tmp[j % 4][i], f[scale_at(j)], acc[n][m][i]);
             // kept here: moved past a branch, they would hold on to their products
             asm volatile("" : "+v"(acc[n][m]));
         };
         auto product = [&](int j) {
+            if (!kOneBlock || j % PH < 2)
+                f[scale_at(j)] = raw[step_of(j) % AR] * ws[kOneBlock ? 0 : channel_of(j)];
             tmp[j % 4] = mfma_block(fb[channel_of(j)], fa[step_of(j) % AR]);
         };
 #pragma unroll
@@ -450,7 +465,7 @@ struct TileF8 {
         for (int i = 0; i < 4; ++i)
             tmp[i] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < AR; ++i)
+        for (int i = 0; i < 4; ++i)
             f[i] = 0.f;
         const bool ragged = g.K % KC != 0;
         const int part = ragged ? kb - 1 : -1;          // the chunk of which K ends inside
@@ -484,21 +499,14 @@ struct TileF8 {
         else
             wait_copies<0>();
         __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            read_b(n, 0);
-        read_a(0, 0, 0);
-        read_a(1, 0, 0);
-        ws = *reinterpret_cast<const float *>(swt);
-        if (c0 == part)
-            clear_past_k(c0);
         // All but the last two steps of a chunk, with act(j) behind product j.
         auto head = [&](int stage, int sbuf, auto &&act) {
 #pragma unroll
+            for (int n = 0; n < WS; ++n)
+                ws[n] = next_ws[n];
+#pragma unroll
             for (int j = 0; j < N - PH; ++j) {
                 const int m = j / PH * 2, i = j % PH;
-                if (i < 2)
-                    f[(m + i) % AR] = raw[(m + i) % AR] * ws;
                 product(j);
                 __builtin_amdgcn_sched_barrier(0);
                 add_up(j >= D ? j - D : N - D + j);     // the first ones are the chunk before's
@@ -513,15 +521,13 @@ struct TileF8 {
 #pragma unroll
             for (int i = 0; i < PH; ++i) {
                 const int j = N - PH + i;
-                if (i < 2)
-                    f[(MT - 2 + i) % AR] = raw[(MT - 2 + i) % AR] * ws;
                 product(j);
                 __builtin_amdgcn_sched_barrier(0);
                 add_up((j - D + N) % N);
                 if (i < 2)
                     read_a(i, next, sbuf);
                 if (i == 1)
-                    ws = *reinterpret_cast<const float *>(swt + sbuf);
+                    read_ws(sbuf);
                 if (i % 2)
                     read_b(i / 2, next);
                 act(i);
@@ -531,15 +537,55 @@ struct TileF8 {
         auto scale_of = [&](int c) {                    // offset of the chunk's scales
             return ((c - c0) & 4 ? SBUF : 0) + ((c - c0) & 3) * 4;
         };
-        head(0, 0, [](int) {});
-        int stage = 0, c = c0;
         const int whole = part >= 0 && part < c1 ? c1 - 1 : c1;
+        int stage = 0, c = c0;
+        // chunk c + 1 has arrived, and every wave holds the rest of chunk c
+        auto arrive = [&](auto left) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_copies<decltype(left)::value>();
+            __syncthreads();
+        };
+        constexpr std::integral_constant<int, (ST - 2) * COPIES> kBehind{};
+        constexpr std::integral_constant<int, 0> kNone{};
+        // the last chunk's copy behind the loop's, where K ends inside it
+        auto copy_last = [&] {
+            if (c + ST < c1) {
+                if (((c + ST - c0) & 3) == 0)
+                    copy_scales(c + ST);
+                copy_part(c + ST);
+            }
+        };
+        // A wave whose rows or channels are all past the end copies its share only.
+        if (wm * (MT * 16) >= count || n0 + wn * WCOLS >= g.N) {
+            for (; c + ST < whole; ++c) {
+                arrive(kBehind);
+                if (((c + ST - c0) & 3) == 0)
+                    copy_scales(c + ST);
+#pragma unroll
+                for (int i = 0; i < COPIES; ++i)
+                    copy_one(i, (uint32_t)((c + ST) * KC), lds0 + stage * STAGE);
+                stage = stage + 1 == ST ? 0 : stage + 1;
+            }
+            for (; c < c1; ++c) {
+                arrive(kNone);
+                copy_last();
+            }
+            if (g.split > 1)
+                meet(g, tile);
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            read_b(n, 0);
+        read_a(0, 0, 0);
+        read_a(1, 0, 0);
+        read_ws(0);
+        if (c0 == part)
+            clear_past_k(c0);
+        head(0, 0, [](int) {});
         for (; c + ST < whole; ++c) {
             const int next = stage + 1 == ST ? 0 : stage + 1, cn = c + ST;
-            // chunk c + 1 has arrived, and every wave holds the rest of chunk c
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            wait_copies<(ST - 2) * COPIES>();
-            __syncthreads();
+            arrive(kBehind);
             if (((cn - c0) & 3) == 0)
                 copy_scales(cn);
             const uint32_t st = lds0 + stage * STAGE;
@@ -557,14 +603,8 @@ struct TileF8 {
         }
         for (;; ++c) {                                  // the last ones
             const int next = stage + 1 == ST ? 0 : stage + 1;
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            wait_copies<0>();
-            __syncthreads();
-            if (c + ST < c1) {                          // the part of a chunk
-                if (((c + ST - c0) & 3) == 0)
-                    copy_scales(c + ST);
-                copy_part(c + ST);
-            }
+            arrive(kNone);
+            copy_last();
             const int sbuf = scale_of(c + 1);
             last(next, sbuf, [](int) {});               // past the end: values that nobody uses
             if (c + 1 == c1)
@@ -582,6 +622,23 @@ struct TileF8 {
                         lds + wave * REGION);
     }
 
+    // Counts the workgroup among its tile's, once all its waves' sums have arrived;
+    // whether it is the last.  Every wave of it comes here.
+    static __device__ __forceinline__ bool meet(const GemmFp8Args &g, int tile)
+    {
+        __shared__ int s_count;
+        wait_copies<0>();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int32_t *count = g.counters + tile;
+            s_count = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (s_count == g.split - 1)
+                __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        return s_count == g.split - 1;
+    }
+
     // Split K: every workgroup of a tile leaves its sums in the workspace and
     // counts itself; the last one adds them up in the order of the slices and
     // writes the tile (true), so nobody waits and no order of arrival shows.  The
@@ -590,7 +647,6 @@ struct TileF8 {
     static __device__ __forceinline__ bool join(const GemmFp8Args &g, v4f (&acc)[NT][MT], int tile,
                                                 int slice)
     {
-        __shared__ int s_count;
         constexpr int PER = NT * MT * 2 * 64 * NW;         // 8-byte words of a tile's sums
         uint64_t *sums = reinterpret_cast<uint64_t *>(g.partial) + (size_t)tile * g.split * PER;
         const int at = (int)(threadIdx.x >> 6) * (NT * MT * 2 * 64) + (int)(threadIdx.x & 63);
@@ -606,16 +662,7 @@ struct TileF8 {
                     __hip_atomic_store(own + ((n * MT + m) * 2 + h) * 64, v, __ATOMIC_RELAXED,
                                        __HIP_MEMORY_SCOPE_AGENT);
                 }
-        wait_copies<0>();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int32_t *count = g.counters + tile;
-            s_count = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (s_count == g.split - 1)
-                __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        __syncthreads();
-        if (s_count != g.split - 1)
+        if (!meet(g, tile))
             return false;
         for (int i = 0; i < g.split; ++i) {
             const uint64_t *one = sums + (size_t)i * PER + at;
@@ -649,10 +696,16 @@ struct TileF8 {
     {
         constexpr int ROW = WCOLS * sizeof(T), PIECES = ROW / 16, EPP = 16 / sizeof(T);
         constexpr int MP = MT < 2 ? MT : 2;   // 16-row steps a pass
-        static_assert(MT % MP == 0 && PIECES >= 2 && MP * 16 * ROW <= REGION, "passes fit");
+        // rows of 2, 4, 8 or 16 pieces are swizzled, others lie a piece further apart
+        constexpr bool kSwizzled = (PIECES & (PIECES - 1)) == 0;
+        constexpr int PITCH = kSwizzled ? ROW : ROW + 16;
+        static_assert(MT % MP == 0 && PIECES >= 2 && MP * 16 * PITCH <= REGION, "passes fit");
         static_assert(MP * 16 * PIECES % 64 == 0, "whole stores");
         auto spread = [](int row) {
-            return PIECES >= 8 ? (row >> 1) & 7 : PIECES >= 4 ? (row >> 2) & 3 : (row >> 3) & 1;
+            return !kSwizzled ? 0
+                   : PIECES >= 8 ? (row >> 1) & 7
+                   : PIECES >= 4 ? (row >> 2) & 3
+                                 : (row >> 3) & 1;
         };
         const int lane = threadIdx.x & 63, r = lane & 15, kq = lane >> 4;
 #pragma unroll
@@ -672,7 +725,7 @@ struct TileF8 {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int byte = (n * 16 + kq * 4) * (int)sizeof(T);
-                    char *at = region + row * ROW + (((byte >> 4) ^ spread(row)) << 4) + (byte & 15);
+                    char *at = region + row * PITCH + (((byte >> 4) ^ spread(row)) << 4) + (byte & 15);
                     Out4<T> v;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -694,7 +747,7 @@ struct TileF8 {
             for (int i = 0; i < STEPS; ++i) {
                 const int id = i * 64 + lane, row = id / PIECES, c = id % PIECES;
                 const int t = t0 + p * MP * 16 + row, n = n0 + c * EPP;
-                const v4i v = *reinterpret_cast<const v4i *>(region + row * ROW +
+                const v4i v = *reinterpret_cast<const v4i *>(region + row * PITCH +
                                                              ((c ^ spread(row)) << 4));
                 store_piece<T>(g, t, t_end, n, v);
             }
@@ -860,9 +913,13 @@ hipError_t launch_grouped_tile(const GemmFp8Args &g, int out_dtype, hipStream_t 
 // and the copies write each once, at 128 bytes a cycle.  128 x 64 a wave (256 x
 // 256) makes that as long as the MFMAs (2048 cycles a block; about 2700 measured),
 // 64 x 64 (128 x 256) longer, 64 x 32 twice as long.  The small tiles are for few
-// rows: they cover them with more CUs.  Two workgroups of 128 x 128 with four waves a
+// rows: they cover them with more CUs.  A wave whose rows or channels are all past the
+// end only copies, so that a part of a tile costs less (E = 256, 65536 rows, N = K =
+// 4096: 1588 -> 1498 us).  Two workgroups of 128 x 128 with four waves a
 // CU do more than one with eight (T = 8192, N = K = 4096: 154 against 182 us),
-// one does less (1024: 28.0 against 22.7).
+// one does less (1024: 28.0 against 22.7).  128 x 192 is for sizes that 128 x 256 would
+// leave in part idle (K = 4096: T = 2048, N = 2057 38.2 -> 33.6 us; 1500, 3000 31.2 -> 27.4;
+// 1280, 4096 32.1 -> 29.1).
 struct TileCost {
     int bm, bn;
     float once, few, all, two, more;
@@ -871,9 +928,10 @@ constexpr TileCost kTiles[] = {
     {256, 256, 6.1f, 1.09f, 1.84f, 0.f, 3.6f},   {128, 256, 5.3f, 0.65f, 1.02f, 0.f, 5.2f},
     {128, 128, 3.4f, 0.67f, 0.87f, 1.14f, 1.5f}, {64, 128, 3.7f, 0.35f, 0.42f, 0.69f, 0.74f},
     {64, 64, 3.2f, 0.32f, 0.36f, 0.46f, 0.82f},  {128, 128, 4.1f, 0.43f, 0.63f, 0.f, 2.5f},
+    {128, 192, 4.8f, 0.40f, 0.82f, 0.f, 3.6f},
 };
-constexpr int kTileCount = 6;
-constexpr int kGroupedTiles = 5;    // the last one is for a CU each: grouped products fill them
+constexpr int kTileCount = 7;
+constexpr int kGroupedTiles = 5;    // the others are for one tile a CU: grouped products have more
 constexpr int kMaxSplit = 16;
 constexpr size_t kCounterBytes = MOE_WNA16_GEMM_SYNC_BYTES;
 
@@ -888,8 +946,8 @@ hipError_t with_tile(int i, F &&f)
     case 3: return f(TileF8<64, 128, 1, 4, 3>{});
     case 4: return f(TileF8<64, 64, 1, 4, 3>{});
     default:
-        if constexpr (COUNT > 5)
-            return f(TileF8<128, 128, 2, 4, 3>{});
+        if constexpr (COUNT > kGroupedTiles)
+            return i == 5 ? f(TileF8<128, 128, 2, 4, 3>{}) : f(TileF8<128, 192, 2, 4, 3>{});
         return hipErrorInvalidValue;
     }
 }
