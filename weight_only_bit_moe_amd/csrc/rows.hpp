@@ -43,8 +43,8 @@ __device__ __forceinline__ void load8(const T *p, int left, float (&f)[8])
         f[j] = to_float(t.v[j]);
 }
 
-// 16 bytes past the caches' replacement order (NT): for outputs larger than they are.
-typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
+// 16 bytes at any element, past the caches' replacement order (NT): for outputs larger than they are.
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void store_past(void *p, Words4 v)
 {
     __builtin_nontemporal_store(v, static_cast<Words4 *>(p));
