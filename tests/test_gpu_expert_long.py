@@ -1,5 +1,6 @@
-"""Operators for experts in 8-bit floating point on tensors whose bytes pass 2^32: the rows behind that
-place are what they would be in a small tensor, and the first ones too."""
+"""Operators for experts in 8-bit floating point on long inputs: tensors whose bytes pass 2^32, where the
+rows behind that place are what they would be in a small tensor, and the first ones too; and sorts of many
+pairs."""
 import pytest
 import torch
 
@@ -116,6 +117,26 @@ def test_sort_and_its_gradient(M):
     s["x"].backward(d)
     exact, terms = rows.double().sum(1), rows.double().abs().sum(1)
     close(x.grad[at(t)].cpu(), exact, (k - 1) * R.U * terms + R.half_step(BF) * 1.001 * exact.abs() + R.smallest(BF))
+
+
+@pytest.mark.parametrize("T,k", [(8193, 8), (70_000, 1), (20_011, 64), (200_000, 6)])
+@pytest.mark.parametrize("E", [1, 64, 65, 1000])
+def test_sort_of_many_pairs(M, T, k, E):
+    H = 24
+    ids = torch.randint(-2, E + 2, (T, k), generator=gen(T + E), dtype=torch.int32).cuda()
+    x = torch.arange(T * H, device="cuda", dtype=torch.float32).view(T, H)
+    s = M.sort_tokens(ids, E, x)
+    flat = ids.view(-1).long()
+    here = (flat >= 0) & (flat < E)
+    order = torch.sort(torch.where(here, flat, E), stable=True)[1]
+    n = int(here.sum())
+    counts = torch.bincount(flat[here], minlength=E)
+    assert torch.equal(s["offsets"].long(), torch.cat([counts.new_zeros(1), counts.cumsum(0)]))
+    assert torch.equal(s["tokens"][:n].long(), order[:n] // k) and bool((s["tokens"][n:] == -1).all())
+    slots = torch.full_like(flat, -1)
+    slots[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(s["slots"].view(-1).long(), slots)
+    assert torch.equal(s["x"][:n], x[order[:n] // k])
 
 
 def test_combine_and_its_gradient(M):

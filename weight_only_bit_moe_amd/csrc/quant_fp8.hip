@@ -13,7 +13,9 @@
 //
 // One pass over memory: 16 lanes hold a block, 8 elements each, and take its
 // maximum by lane permutes; every input is read once and every output written
-// once.
+// once.  Memory bounds it: T = 8192, I = 2048 SwiGLU (84 MB) 20 us = 4.2 TB/s; T = 2047, K =
+// 4096 (25 MB, most of it from the last-level cache or on its way there) 6.1 us with its
+// launch = 4.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "moe_wna16.h"

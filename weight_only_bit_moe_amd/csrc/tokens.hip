@@ -6,11 +6,14 @@
 // every workgroup compares its own tokens' pairs with all ids: one launch, and
 // the tokens' rows are on their way meanwhile.  More pairs are counted in chunks
 // first; a workgroup then needs the counts of all chunks and the ids of its own.
-// Past kManyChunks chunks a launch in between turns the counts into the first
-// slot of each (chunk, expert).  No order of any atomic matters: they only count.
+// Past kManyChunks chunks a launch in between adds up the counts of the chunks before.
+// No order of any atomic matters: they only count.
 //
 // The rows are the bulk: each token's row is read once, into registers, and
-// written to its topk places.
+// written to its topk places, so memory's write rate bounds it.  T = 4096, k = 8, H =
+// 4096 (302 MB) 64 us = 4.7 TB/s, of which the slots take 9 on their own; T = 65536, k =
+// 8, H = 1024 (1.2 GB) 237 us = 5.1 TB/s; T = 64, k = 6, H = 4096 4 us, most of it the launch
+// and one trip to memory for the ids and one for the rows.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -24,9 +27,13 @@ namespace wna16 {
 
 namespace {
 
+// One launch against two, sort alone (256 experts): 4096 pairs 5.5 and 6.5 us, 8192 pairs 11.1
+// and 6.9.
 constexpr int kOneLaunch = 4096;        // pairs
 constexpr int kOwn = 64;                // pairs placed by one workgroup, at least one token's
 constexpr int kChunk = 1024;            // pairs of a counted chunk, about
+// Two launches against three: 32 chunks (256 experts) 9.1 and 10.3 us, 64 (both 64 and 256)
+// 11.4 either way, 128 20.0 and 12.4.
 constexpr int kManyChunks = 64;
 constexpr int kThreads = 256;
 constexpr int kMaxExperts = 1024;
@@ -94,13 +101,15 @@ __global__ void __launch_bounds__(kThreads) count_kernel(SortArgs a)
         a.counts[(size_t)blockIdx.x * a.E + e] = count[e];
 }
 
-// Then: counts of chunks -> first slot of each (chunk, expert), and the offsets.
-// A workgroup of 1024: each expert's chunks in 1024 / span runs.
-__global__ void __launch_bounds__(1024) first_slots_kernel(SortArgs a, int chunks, int span)
+// Then: each expert's counts -> the pairs of the chunks before, and all of them behind the
+// last chunk's.  A workgroup has 64 experts, each one's chunks in 16 runs.  (All experts
+// in one workgroup: T = 65536, k = 8 the sort alone took 40.7 us with 256 experts, 103 with
+// 1024.)
+__global__ void __launch_bounds__(1024) before_kernel(SortArgs a, int chunks)
 {
-    __shared__ int run[1024], total[kMaxExperts];
-    const int e = (int)threadIdx.x % span, seg = (int)threadIdx.x / span, segs = 1024 / span;
-    const int per = (chunks + segs - 1) / segs;
+    __shared__ int run[16][64];
+    const int lane = threadIdx.x & 63, seg = threadIdx.x >> 6, e = (int)blockIdx.x * 64 + lane;
+    const int per = (chunks + 15) / 16;
     const int c0 = seg * per, c1 = c0 + per < chunks ? c0 + per : chunks;
     int sum = 0;
     if (e < a.E) {
@@ -108,61 +117,28 @@ __global__ void __launch_bounds__(1024) first_slots_kernel(SortArgs a, int chunk
         for (int c = c0; c < c1; ++c)
             sum += a.counts[(size_t)c * a.E + e];
     }
-    run[threadIdx.x] = sum;
+    run[seg][lane] = sum;
     __syncthreads();
-    if (threadIdx.x < (unsigned)a.E) {
-        int t = 0;
-        for (int s = 0; s < segs; ++s) {
-            const int v = run[s * span + threadIdx.x];
-            run[s * span + threadIdx.x] = t;
-            t += v;
-        }
-        total[threadIdx.x] = t;
+    if (e >= a.E)
+        return;
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        before += i < seg ? run[i][lane] : 0;
+        all += run[i][lane];
     }
-    __syncthreads();
-    // exclusive scan of the totals by the first wave, 16 experts a lane
-    if (threadIdx.x < 64) {
-        int v[16], s = 0;
+    if (seg == 0)
+        a.counts[(size_t)chunks * a.E + e] = all;
+    for (int c = c0; c < c1; c += 8) {                  // eight loads on their way at a time
+        int n[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int at = (int)threadIdx.x * 16 + i;
-            v[i] = at < a.E ? total[at] : 0;
-            s += v[i];
-        }
-        int incl = s;
+        for (int i = 0; i < 8; ++i)
+            n[i] = c + i < c1 ? a.counts[(size_t)(c + i) * a.E + e] : 0;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if ((int)threadIdx.x >= d)
-                incl += o;
-        }
-        int before = incl - s;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int at = (int)threadIdx.x * 16 + i;
-            if (at < a.E) {
-                total[at] = before;
-                a.offsets[at] = before;
-            }
-            before += v[i];
-        }
-        if (threadIdx.x == 63)
-            a.offsets[a.E] = before;
-    }
-    __syncthreads();
-    if (e < a.E) {
-        int slot = total[e] + run[threadIdx.x];
-        for (int c = c0; c < c1; c += 8) {          // eight loads on their way at a time
-            int n[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                n[i] = c + i < c1 ? a.counts[(size_t)(c + i) * a.E + e] : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (c + i < c1)
-                    a.counts[(size_t)(c + i) * a.E + e] = slot;
-                slot += n[i];
-            }
+        for (int i = 0; i < 8; ++i) {
+            if (c + i < c1)
+                a.counts[(size_t)(c + i) * a.E + e] = before;
+            before += n[i];
         }
     }
 }
@@ -285,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) sort_one_kernel(SortArgs a)
 }
 
 // Many pairs: a workgroup's tokens get their slots, and its part of their columns is
-// copied.  FIRST: the counts have been turned into first slots and offsets.
-template <bool FIRST, bool NT>
+// copied.  BEFORE: before_kernel has added up the counts.
+template <bool BEFORE, bool NT>
 __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a, int chunks)
 {
     __shared__ int base[kMaxExperts], earlier[kMaxExperts], own[kOwn], slot[kOwn];
@@ -295,9 +271,9 @@ __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a, int chunks)
     const int P = a.T * a.topk, p0 = t0 * a.topk, n = n_tokens * a.topk;
     const int chunk = t0 / a.chunk, first = chunk * a.chunk * a.topk;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        if constexpr (FIRST) {
-            base[e] = a.counts[(size_t)chunk * a.E + e];
-            earlier[e] = 0;
+        if constexpr (BEFORE) {
+            base[e] = a.counts[(size_t)chunks * a.E + e];
+            earlier[e] = a.counts[(size_t)chunk * a.E + e];
         } else {
             int all = 0, mine = 0;
             for (int c = 0; c < chunks; c += 8) {           // eight loads on their way at a time
@@ -324,11 +300,7 @@ __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a, int chunks)
             atomicAdd(&earlier[id], 1);
     }
     __syncthreads();
-    int total = 0;
-    if constexpr (FIRST)
-        total = a.offsets[a.E];
-    else
-        total = exclusive_scan(base, a.E);
+    const int total = exclusive_scan(base, a.E);
     if ((int)threadIdx.x < n) {
         const int id = own[threadIdx.x];
         int s = -1;
@@ -345,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) place_kernel(SortArgs a, int chunks)
         }
     }
     if (blockIdx.y == 0) {
-        if (!FIRST && blockIdx.x == 0) {
+        if (blockIdx.x == 0) {
             for (int e = threadIdx.x; e < a.E; e += kThreads)
                 a.offsets[e] = base[e];
             if (threadIdx.x == 0)
@@ -386,7 +358,7 @@ size_t sort_workspace(int T, int topk, int E)
     if ((long long)T * topk <= kOneLaunch)
         return 0;
     const int per = tokens_a_chunk(topk, tokens_a_group(T, topk));
-    return (size_t)((T + per - 1) / per) * E * sizeof(int32_t);
+    return ((size_t)((T + per - 1) / per) + 1) * E * sizeof(int32_t);   // and all chunks' sums
 }
 
 hipError_t launch_sort_tokens(const SortArgs &args, hipStream_t stream)
@@ -419,10 +391,7 @@ hipError_t launch_sort_tokens(const SortArgs &args, hipStream_t stream)
     if (chunks <= kManyChunks)
         return launch(nt ? place_kernel<false, true> : place_kernel<false, false>, grid, kThreads,
                       stream, a, chunks);
-    int span = 64;
-    while (span < a.E)
-        span *= 2;
-    e = launch(first_slots_kernel, dim3(1), 1024, stream, a, chunks, span);
+    e = launch(before_kernel, dim3((unsigned)((a.E + 63) / 64)), 1024, stream, a, chunks);
     if (e != hipSuccess)
         return e;
     return launch(nt ? place_kernel<true, true> : place_kernel<true, false>, grid, kThreads, stream, a,
@@ -483,7 +452,9 @@ __global__ void __launch_bounds__(1024) combine_kernel(CombineArgs a)
 // The gradients:  dy[slot[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[slot[t][j]]>.
 // A workgroup owns a token and holds its row of dout; each row of y is read and
 // each row of dy written once.  Workgroups behind the tokens clear the rows of dy
-// that no token has.
+// that no token has.  Bytes bound it: T = 4096, k = 8, H = 4096 (570 MB) 99 us = 5.7 TB/s;
+// combine_kernel there (302 MB) 56 us = 5.4 TB/s.  The dot products are FP32: eight elements
+// in order, then the rows' pieces, lanes and waves in a fixed order.
 constexpr int kClearGroups = 256;
 
 template <class T, int R, bool NT>
