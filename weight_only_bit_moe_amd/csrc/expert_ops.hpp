@@ -15,6 +15,8 @@ struct QuantArgs {
     long long x_stride, q_stride, s_stride;     // elements between rows
     int T, n;
     int blocks;                                 // a row's, set by the launch
+    int shift;                                  // id / blocks for ids, set by the launch
+    uint32_t magic;
     float alpha, beta, clamp;                   // SwiGLU; clamp = +inf: none
     uint8_t *q;
     float *scale;

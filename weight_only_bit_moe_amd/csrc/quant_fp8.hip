@@ -13,9 +13,10 @@
 //
 // One pass over memory: 16 lanes hold a block, 8 elements each, and take its
 // maximum by lane permutes; every input is read once and every output written
-// once.  Memory bounds it: T = 8192, I = 2048 SwiGLU (84 MB) 20 us = 4.2 TB/s; T = 2047, K =
-// 4096 (25 MB, most of it from the last-level cache or on its way there) 6.1 us with its
-// launch = 4.1 TB/s.
+// once.  Memory bounds it, and the SwiGLU's arithmetic nearly as much (the vector units
+// were 90 % busy before places were worked out for a wave, and NaNs looked for beside the
+// clamps and maxima): T = 8192, I = 2048 SwiGLU (84 MB) 21.4 -> 19.2 us = 4.4 TB/s; T = 2047, K =
+// 4096 (25 MB) 6.6 -> 6.2 us = 4.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "moe_wna16.h"
@@ -48,47 +49,93 @@ __device__ __forceinline__ Codes8 to_e4m3(const float (&v)[8], float mult)
     return Codes8{(uint32_t)lo, (uint32_t)hi};
 }
 
+// The larger of top, |a| and |b|, none of them a NaN that counts.
+__device__ __forceinline__ float largest(float top, float a, float b)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(top), "v"(a), "v"(b));
+    return r;
+}
+
+// Where a block's elements, codes and scale are: elements from the start of x, q
+// and scale.
+struct Place {
+    long long x, q, s;
+    int c;                      // the lane's first element in its row
+    bool here;
+};
+
+// A wave has four blocks in turn.  A row of four or more ends at most once among them:
+// its place is worked out once for the wave, and a lane behind the end adds a stride.
+__device__ __forceinline__ Place place_of(const QuantArgs &a)
+{
+    const int lane = threadIdx.x & 63;
+    const uint32_t id0 =
+        (uint32_t)__builtin_amdgcn_readfirstlane((int)(blockIdx.x * 16u + (threadIdx.x >> 6) * 4u));
+    const uint32_t n = (uint32_t)a.blocks, sub = (uint32_t)lane >> 4;
+    Place p;
+    if (n >= 4) {
+        // id0 / n, as set by the launch
+        const uint32_t row0 = __umulhi(id0, a.magic) >> a.shift, b0 = id0 - row0 * n;
+        const bool next = b0 + sub >= n;
+        const uint32_t b = b0 + sub - (next ? n : 0u);
+        p.c = (int)b * 128 + (lane & 15) * 8;
+        p.x = (long long)row0 * a.x_stride + (next ? a.x_stride : 0ll) + p.c;
+        p.q = (long long)row0 * a.q_stride + (next ? a.q_stride : 0ll) + p.c;
+        p.s = (long long)row0 * a.s_stride + (next ? a.s_stride : 0ll) + b;
+        p.here = row0 + (next ? 1u : 0u) < (uint32_t)a.T;
+    } else {
+        const uint32_t row = (id0 + sub) / n, b = id0 + sub - row * n;
+        p.c = (int)b * 128 + (lane & 15) * 8;
+        p.x = (long long)row * a.x_stride + p.c;
+        p.q = (long long)row * a.q_stride + p.c;
+        p.s = (long long)row * a.s_stride + b;
+        p.here = row < (uint32_t)a.T;
+    }
+    return p;
+}
+
 template <class T, bool SWIGLU>
 __global__ void __launch_bounds__(256) quant_fp8_kernel(QuantArgs a)
 {
     // 16 lanes a block: those of a row's last block past its end hold zeros
-    const uint32_t id = blockIdx.x * 16u + (threadIdx.x >> 4);
-    const uint32_t row = id / (uint32_t)a.blocks, b = id - row * (uint32_t)a.blocks;
-    if (row >= (uint32_t)a.T)
+    const Place at = place_of(a);
+    if (!at.here)
         return;                                     // whole rows of 16 lanes
-    const int c = (int)b * 128 + (int)(threadIdx.x & 15) * 8, left = a.n - c;
-    const T *x = static_cast<const T *>(a.x) + (long long)row * a.x_stride + c;
+    const int left = a.n - at.c;
+    const T *x = static_cast<const T *>(a.x) + at.x;
     float v[8];
     load8(x, left, v);
+    bool odd = false;                               // a NaN
     if constexpr (SWIGLU) {
         float u[8];
         load8(x + a.n, left, u);
         const bool clamped = a.clamp < INFINITY;
+        if (clamped) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float gc = v[j], uc = u[j];
-            if (clamped) {      // comparisons that keep a NaN (fminf would drop it)
-                gc = gc > a.clamp ? a.clamp : gc;
-                uc = uc > a.clamp ? a.clamp : uc;
-                uc = uc < -a.clamp ? -a.clamp : uc;
+            for (int j = 0; j < 8; ++j) {           // these drop a NaN
+                odd |= __builtin_isunordered(v[j], u[j]);
+                v[j] = __builtin_amdgcn_fmed3f(v[j], -INFINITY, a.clamp);
+                u[j] = __builtin_amdgcn_fmed3f(u[j], -a.clamp, a.clamp);
             }
-            v[j] = gc * sigmoid(a.alpha * gc) * (uc + a.beta);
         }
-    }
-    uint32_t top = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        top = larger(top, magnitude(v[j]));
-    top = each_row_max(top);
-    const bool fine = top < kInfBits;
-    if (!fine) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = 0.f;
+            v[j] = v[j] * sigmoid(a.alpha * v[j]) * (u[j] + a.beta);
     }
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        odd |= __builtin_isunordered(v[j], v[j + 1]);
+        most = largest(most, v[j], v[j + 1]);
+    }
+    const uint32_t top = each_row_max(odd ? kInfBits : __float_as_uint(most));
+    const bool fine = top < kInfBits;
     const uint32_t e = scale_exponent(fine ? top : 0u);
-    const Codes8 q = to_e4m3(v, __uint_as_float((254u - e) << 23));
-    uint8_t *o = a.q + (long long)row * a.q_stride + c;
+    Codes8 q = to_e4m3(v, __uint_as_float((254u - e) << 23));
+    q.lo = fine ? q.lo : 0u;
+    q.hi = fine ? q.hi : 0u;
+    uint8_t *o = a.q + at.q;
     if (left >= 8) {
         *reinterpret_cast<Codes8 *>(o) = q;
     } else {
@@ -98,7 +145,7 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(QuantArgs a)
                 o[j] = (uint8_t)((j < 4 ? q.lo : q.hi) >> (8 * (j & 3)));
     }
     if ((threadIdx.x & 15) == 0)
-        a.scale[(long long)row * a.s_stride + b] = __uint_as_float(fine ? e << 23 : 0x7fc00000u);
+        a.scale[at.s] = __uint_as_float(fine ? e << 23 : 0x7fc00000u);
 }
 
 template <bool SWIGLU>
@@ -118,6 +165,11 @@ hipError_t launch_quant_fp8(const QuantArgs &args, bool swiglu, int dtype, hipSt
 {
     QuantArgs a = args;
     a.blocks = (a.n + 127) / 128;
+    // id / blocks = id * magic / 2^(32 + shift): 2^shift < blocks <= 2^(shift + 1) and an
+    // excess of magic * blocks over 2^(32 + shift) below blocks, so exact for id < 2^31
+    while ((2 << a.shift) < a.blocks)
+        ++a.shift;
+    a.magic = (uint32_t)(((1ull << (32 + a.shift)) + a.blocks - 1) / a.blocks);
     return swiglu ? launch_quant<true>(a, dtype, stream) : launch_quant<false>(a, dtype, stream);
 }
 
