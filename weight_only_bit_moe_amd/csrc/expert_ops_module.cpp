@@ -1,8 +1,13 @@
 // The operators for experts in 8-bit floating point in the Python module
 // _block_ops: checks, allocation and the library call, as for the operators
-// around the layer.  Gradients are made above this (expert_ops.py): what is here
-// computes on values.
+// around the layer; and the graph nodes of sort and combine.  A node's gradient runs
+// on torch's own thread without the interpreter: written in Python, small
+// gradients waited for the interpreter's lock (forward and backward of 32 tokens: sort
+// 86 -> 49 us, combine 73 -> 52, where torch's product by two takes 43).
 #include "torch_module.hpp"
+
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 
 namespace {
 
@@ -177,6 +182,136 @@ const at::Tensor &expert_ids(PyObject *o, const char *name)
     return t;
 }
 
+// ---- gradients: without the interpreter's lock, on arguments checked before ------
+
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+int code_of(at::ScalarType t)
+{
+    return t == at::kBFloat16 ? MOE_WNA16_BF16 : t == at::kHalf ? MOE_WNA16_FP16 : MOE_WNA16_FP32;
+}
+
+template <class F>
+void launch_plain(const char *name, c10::Device dev, F &&f)
+{
+    const c10::DeviceGuard guard(dev);
+    const int st = f(c10::hip::getCurrentHIPStream(dev.index()).stream());
+    TORCH_CHECK(st == MOE_WNA16_OK, name, ": status ", st);
+}
+
+// A gradient with rows that the kernels read (the graph also hands over expanded ones).
+at::Tensor with_rows(const at::Tensor &d)
+{
+    return (d.size(1) <= 1 || d.stride(1) == 1) && (d.size(0) <= 1 || d.stride(0) >= d.size(1))
+               ? d
+               : d.contiguous();
+}
+int64_t row_stride(const at::Tensor &d) { return d.size(0) <= 1 ? d.size(1) : d.stride(0); }
+
+// Results of a gradient carry no graph of their own: where one is asked for, they say so
+// when it is used.
+variable_list once(variable_list grads)
+{
+    if (!at::GradMode::is_enabled())
+        return grads;
+    for (at::Tensor &g : grads)
+        if (g.defined()) {
+            auto error = std::make_shared<torch::autograd::DelayedError>(
+                "the gradients of sort_tokens and combine_tokens have no gradient", 1);
+            g = (*error)({g.detach().set_requires_grad(true)})[0];
+        }
+    return grads;
+}
+
+struct Sorted {
+    at::Tensor tokens, slots, offsets, x;       // x may be undefined
+};
+
+struct SortNode : torch::autograd::Function<SortNode> {
+    // the values have been computed: what is left is their place in the graph
+    static variable_list forward(AutogradContext *ctx, const at::Tensor &, const Sorted *r)
+    {
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({r->slots});
+        ctx->mark_non_differentiable({r->tokens, r->slots, r->offsets});
+        return {r->tokens, r->slots, r->offsets, r->x};
+    }
+    static variable_list backward(AutogradContext *ctx, variable_list grads)
+    {
+        if (!grads[3].defined())
+            return {at::Tensor(), at::Tensor()};
+        const at::AutoDispatchBelowADInplaceOrView below;
+        const at::Tensor d = with_rows(grads[3]), slots = ctx->get_saved_variables()[0];
+        const int64_t T = slots.size(0), H = d.size(1);
+        at::Tensor dx = empty({T, H}, d.scalar_type(), d.device());
+        launch_plain("moe_wna16_combine_tokens", d.device(), [&](hipStream_t s) {
+            return lib.combine_tokens(d.data_ptr(), (const int32_t *)slots.data_ptr(), nullptr,
+                                      nullptr, (int)T, (int)slots.size(1), (int)H, (int)d.size(0),
+                                      row_stride(d), H, H, code_of(d.scalar_type()), dx.data_ptr(), s);
+        });
+        return once({dx, at::Tensor()});
+    }
+};
+
+struct Combined {
+    at::Tensor slots, offsets, out;             // offsets may be undefined
+    bool y, weights, addend;                    // which require a gradient
+};
+
+struct CombineNode : torch::autograd::Function<CombineNode> {
+    static variable_list forward(AutogradContext *ctx, const at::Tensor &y,
+                                 const std::optional<at::Tensor> &weights,
+                                 const std::optional<at::Tensor> &, const Combined *c)
+    {
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({c->weights ? y : at::Tensor(), c->slots,
+                                weights ? *weights : at::Tensor(), c->offsets});
+        ctx->saved_data["rows"] = y.size(0);
+        ctx->saved_data["wanted"] = (int64_t)(c->y + 2 * c->weights + 4 * c->addend);
+        return {c->out};
+    }
+    static variable_list backward(AutogradContext *ctx, variable_list grads)
+    {
+        if (!grads[0].defined())
+            return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+        const int64_t wanted = ctx->saved_data["wanted"].toInt(), R = ctx->saved_data["rows"].toInt();
+        const variable_list saved = ctx->get_saved_variables();
+        const at::Tensor &y = saved[0], &slots = saved[1], &weights = saved[2], &offsets = saved[3];
+        at::Tensor dy, dw;
+        if (wanted & 3) {
+            const at::AutoDispatchBelowADInplaceOrView below;
+            const at::Tensor d = with_rows(grads[0]);
+            const int64_t T = slots.size(0), k = slots.size(1), H = d.size(1);
+            const int32_t *used = nullptr;
+            if (wanted & 1) {
+                dy = empty({R, H}, d.scalar_type(), d.device());
+                if (offsets.defined())
+                    used = (const int32_t *)offsets.data_ptr() + offsets.numel() - 1;
+                else
+                    dy.zero_();                 // rows that no slot names
+            }
+            if (wanted & 2)
+                dw = empty({T, k}, at::kFloat, d.device());
+            launch_plain("moe_wna16_combine_tokens_grad", d.device(), [&](hipStream_t s) {
+                return lib.combine_tokens_grad(
+                    d.data_ptr(), dw.defined() ? y.data_ptr() : nullptr,
+                    (const int32_t *)slots.data_ptr(),
+                    weights.defined() ? (const float *)weights.data_ptr() : nullptr, used, (int)T,
+                    (int)k, (int)H, (int)R, row_stride(d), dw.defined() ? row_stride(y) : H, H,
+                    code_of(d.scalar_type()), dy.defined() ? dy.data_ptr() : nullptr,
+                    dw.defined() ? (float *)dw.data_ptr() : nullptr, s);
+            });
+        }
+        variable_list r = once({dy, dw});
+        return {r[0], r[1], wanted & 4 ? grads[0] : at::Tensor(), at::Tensor()};
+    }
+};
+
+// ---- sort and combine ------------------------------------------------------------
+
+// GRAPH: the result is part of x's graph.
+template <bool GRAPH>
 PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
 {
     PyObject *const names[] = {n_ids, n_experts, n_x, n_out};
@@ -190,7 +325,8 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     if (k < 1)
         fail(PyExc_ValueError, "ids must name at least one expert a token");
     ensure_library();
-    at::Tensor xs;
+    Sorted r;
+    at::Tensor &xs = r.x;
     const void *xp = nullptr;
     int64_t H = 0, xst = 0, xsst = 0;
     int code = MOE_WNA16_BF16;
@@ -207,8 +343,10 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     } else if (p.v[3]) {
         fail(PyExc_ValueError, "out without x");
     }
-    at::Tensor tokens = empty({P}, at::kInt, dev), slots = empty({T, k}, at::kInt, dev);
-    at::Tensor offsets = empty({(int64_t)E + 1}, at::kInt, dev), ws;
+    at::Tensor &tokens = r.tokens, &slots = r.slots, &offsets = r.offsets, ws;
+    tokens = empty({P}, at::kInt, dev);
+    slots = empty({T, k}, at::kInt, dev);
+    offsets = empty({(int64_t)E + 1}, at::kInt, dev);
     size_t bytes = 0;
     if (lib.sort_tokens_workspace_size((int)T, (int)k, E, &bytes) == MOE_WNA16_OK && bytes)
         ws = empty({(int64_t)bytes}, at::kByte, dev);
@@ -218,6 +356,10 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
                                (int32_t *)offsets.data_ptr(), xp ? xs.data_ptr() : nullptr, xsst,
                                bytes ? ws.data_ptr() : nullptr, bytes, s);
     });
+    if constexpr (GRAPH) {
+        const variable_list v = SortNode::apply(tensor(p.v[2], "x"), (const Sorted *)&r);
+        r = Sorted{v[0], v[1], v[2], v[3]};
+    }
     PyObject *d = PyDict_New();
     if (!d)
         throw Raised{};
@@ -234,10 +376,12 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     return d;
 }
 
+// GRAPH: the result is part of the graphs of y, weights and addend.
+template <bool GRAPH>
 PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
 {
-    PyObject *const names[] = {n_y, n_slots, n_weights, n_addend, n_out};
-    const Args<5> p("combine_tokens", names, 3, 2, args, nargs, kw);
+    PyObject *const names[] = {n_y, n_slots, n_weights, n_addend, n_out, n_offsets};
+    const Args<6> p("combine_tokens", names, 3, 2, args, nargs, kw);
     const at::Tensor &y = matrix(p.v[0], "y"), &slots = expert_ids(p.v[1], "slots");
     const int64_t R = y.size(0), H = y.size(1), T = slots.size(0), k = slots.size(1);
     const c10::Device dev = y.device();
@@ -263,61 +407,22 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
                                   (const float *)wp, ap, (int)T, (int)k, (int)H, (int)R, ys, as, os,
                                   code, out.data_ptr(), s);
     });
-    return THPVariable_Wrap(out);
-}
-
-// combine_tokens_grad(dout, y, slots, weights, offsets, R, want_dy, want_dw):
-// (dy or None, dw or None); y may be None where dw is not wanted.
-PyObject *combine_tokens_grad(PyObject *const *args, Py_ssize_t nargs, PyObject *)
-{
-    if (nargs != 8)
-        fail(PyExc_TypeError, "combine_tokens_grad() takes 8 arguments");
-    auto given = [&](int i) { return args[i] == Py_None ? nullptr : args[i]; };
-    const at::Tensor &d = matrix(args[0], "dout"), &slots = expert_ids(args[2], "slots");
-    const int64_t T = d.size(0), H = d.size(1), k = slots.size(1), R = integer(args[5], 0);
-    const bool want_dy = truth(args[6], true), want_dw = truth(args[7], true);
-    const c10::Device dev = d.device();
-    const at::ScalarType dt = d.scalar_type();
-    const int code = dtype_code(dt, "dout");
-    const int64_t ds = rows(d, "dout", {T, H}, dt, dev);
-    check(slots, "slots", {T, k}, at::kInt, dev);
-    const void *yp = nullptr;
-    int64_t ys = H;
-    if (want_dw) {
-        const at::Tensor &y = tensor(args[1], "y");
-        ys = rows(y, "y", {R, H}, dt, dev);
-        yp = y.data_ptr();
-    }
-    const void *wp = optional_flat(given(3), "weights", {T, k}, at::kFloat, dev);
-    const int32_t *used = nullptr;
-    at::Tensor dy, dw;
-    ensure_library();
-    if (want_dy) {
-        dy = empty({R, H}, dt, dev);
-        if (PyObject *o = given(4)) {
-            const at::Tensor &offsets = tensor(o, "offsets");
-            const int64_t n = offsets.numel();
-            if (n < 1)
+    if constexpr (GRAPH) {
+        auto given = [&](int i) {
+            return p.v[i] ? std::optional<at::Tensor>(THPVariable_Unpack(p.v[i])) : std::nullopt;
+        };
+        const std::optional<at::Tensor> w = given(2), add = given(3);
+        Combined c{slots, {}, out, y.requires_grad(), w && w->requires_grad(),
+                   add && add->requires_grad()};
+        if (p.v[5]) {
+            c.offsets = tensor(p.v[5], "offsets");
+            flat(c.offsets, "offsets", {c.offsets.numel()}, at::kInt, dev);
+            if (c.offsets.numel() < 1)
                 fail(PyExc_ValueError, "offsets is empty");
-            used = static_cast<const int32_t *>(flat(offsets, "offsets", {n}, at::kInt, dev)) + n - 1;
-        } else {
-            dy.zero_();                             // rows that no slot names
         }
+        out = CombineNode::apply(y, w, add, (const Combined *)&c)[0];
     }
-    if (want_dw)
-        dw = empty({T, k}, at::kFloat, dev);
-    launch("moe_wna16_combine_tokens_grad", dev, [&](hipStream_t s) {
-        return lib.combine_tokens_grad(d.data_ptr(), yp, (const int32_t *)slots.data_ptr(),
-                                       (const float *)wp, used, (int)T, (int)k, (int)H, (int)R, ds,
-                                       ys, H, code, want_dy ? dy.data_ptr() : nullptr,
-                                       want_dw ? (float *)dw.data_ptr() : nullptr, s);
-    });
-    PyObject *a = want_dy ? THPVariable_Wrap(dy) : Py_NewRef(Py_None);
-    PyObject *b = want_dw ? THPVariable_Wrap(dw) : Py_NewRef(Py_None);
-    PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-    Py_XDECREF(a);
-    Py_XDECREF(b);
-    return r;
+    return THPVariable_Wrap(out);
 }
 
 const char k_quant_fp8[] = R"(quant_fp8(x, *, q=None, scale=None) -> (q, scale)
@@ -366,9 +471,10 @@ PyMethodDef methods[] = {
     {"gemm_fp8", MOE_MODULE_FAST(gemm_fp8), METH_FASTCALL | METH_KEYWORDS, k_gemm_fp8},
     {"gemm_fp8_grouped", MOE_MODULE_FAST(gemm_fp8_grouped), METH_FASTCALL | METH_KEYWORDS,
      k_gemm_fp8_grouped},
-    {"sort_tokens", MOE_MODULE_FAST(sort_tokens), METH_FASTCALL | METH_KEYWORDS, nullptr},
-    {"combine_tokens", MOE_MODULE_FAST(combine_tokens), METH_FASTCALL | METH_KEYWORDS, nullptr},
-    {"combine_tokens_grad", MOE_MODULE_FAST(combine_tokens_grad), METH_FASTCALL | METH_KEYWORDS,
+    {"sort_tokens", MOE_MODULE_FAST(sort_tokens<false>), METH_FASTCALL | METH_KEYWORDS, nullptr},
+    {"sort_tokens_graph", MOE_MODULE_FAST(sort_tokens<true>), METH_FASTCALL | METH_KEYWORDS, nullptr},
+    {"combine_tokens", MOE_MODULE_FAST(combine_tokens<false>), METH_FASTCALL | METH_KEYWORDS, nullptr},
+    {"combine_tokens_graph", MOE_MODULE_FAST(combine_tokens<true>), METH_FASTCALL | METH_KEYWORDS,
      nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

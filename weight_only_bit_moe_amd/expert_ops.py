@@ -13,7 +13,9 @@ allocation and the library call are in the compiled module _block_ops, as for th
 operators around the layer.  The raw entry points take integer device addresses.
 
 sort_tokens and combine_tokens give gradients to x, y, the weights and the addend where they
-require one (once: a gradient's own graph is not made); the others take tensors as values.
+require one (a gradient's own graph is refused); the others take tensors as values.  A step captured
+into a graph has its forward and its backward in the one capture, and no eager graph of the same
+leaves may be alive then: torch ends the process over the stream it was made on.
 """
 from __future__ import annotations
 
@@ -111,25 +113,6 @@ def _wants_grad(*tensors) -> bool:
                                            for t in tensors)
 
 
-def _rows(d: torch.Tensor) -> torch.Tensor:
-    """A gradient with rows that the kernels read (autograd also hands over expanded ones)."""
-    return d if d.stride(1) == 1 and d.stride(0) >= d.shape[1] else d.contiguous()
-
-
-class _SortTokens(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, ids, experts, x):
-        r = _block_ops.sort_tokens(ids, experts, x)
-        ctx.save_for_backward(r["slots"])
-        ctx.mark_non_differentiable(r["tokens"], r["slots"], r["offsets"])
-        return r["tokens"], r["slots"], r["offsets"], r["x"]
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, _tokens, _slots, _offsets, dxs):
-        return None, None, _block_ops.combine_tokens(_rows(dxs), ctx.saved_tensors[0])
-
-
 def sort_tokens(ids: torch.Tensor, experts: int, x: Optional[torch.Tensor] = None, *,
                 out: Optional[torch.Tensor] = None) -> dict:
     """sort_tokens(ids, experts, x=None, *, out=None) -> dict
@@ -147,28 +130,8 @@ def sort_tokens(ids: torch.Tensor, experts: int, x: Optional[torch.Tensor] = Non
     if _wants_grad(x):
         if out is not None:
             raise ValueError("out is given, and x requires a gradient")
-        return dict(zip(("tokens", "slots", "offsets", "x"), _SortTokens.apply(ids, experts, x)))
+        return _block_ops.sort_tokens_graph(ids, experts, x)
     return _block_ops.sort_tokens(ids, experts, x, out=out)
-
-
-class _CombineTokens(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, y, slots, weights, offsets, addend):
-        want_dw = ctx.needs_input_grad[2]
-        ctx.rows = y.shape[0]
-        ctx.save_for_backward(y if want_dw else None, slots, weights, offsets)
-        return _block_ops.combine_tokens(y, slots, weights, addend=addend)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dout):
-        y, slots, weights, offsets = ctx.saved_tensors
-        want_dy, _, want_dw, _, want_add = ctx.needs_input_grad
-        dy = dw = None
-        if want_dy or want_dw:
-            dy, dw = _block_ops.combine_tokens_grad(_rows(dout), y, slots, weights, offsets, ctx.rows,
-                                                    want_dy, want_dw)
-        return dy, None, dw, None, dout if want_add else None
 
 
 def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
@@ -189,9 +152,7 @@ def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch
     if _wants_grad(y, weights, addend):
         if out is not None:
             raise ValueError("out is given, and a gradient is required")
-        if offsets is not None and offsets.device != y.device:
-            raise ValueError(f"offsets is on {offsets.device}, expected {y.device}")
-        return _CombineTokens.apply(y, slots, weights, offsets, addend)
+        return _block_ops.combine_tokens_graph(y, slots, weights, addend=addend, offsets=offsets)
     return _block_ops.combine_tokens(y, slots, weights, addend=addend, out=out)
 
 
@@ -210,7 +171,8 @@ def forward_fp8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w
     swiglu_quant_fp8; the gate and up rows and the experts' rows are rounded to x's type in between.
     No gradient.
 
-    Rows of experts that are elsewhere cost memory and a pass of the activation, but no product."""
+    Rows of experts that are elsewhere cost memory and a pass of the activation, but no product.
+    T * k up to 2^21, T * H below 2^32."""
     q, scale = quant_fp8(x) if codes is None else codes
     s = _block_ops.sort_tokens(topk_ids, w13.shape[0])
     gu = gemm_fp8_grouped(q, scale, w13, w13_scale, s["offsets"], rows=s["tokens"], out_dtype=x.dtype)
