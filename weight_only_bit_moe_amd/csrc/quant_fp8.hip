@@ -13,10 +13,10 @@
 //
 // One pass over memory: 16 lanes hold a block, 8 elements each, and take its
 // maximum by lane permutes; every input is read once and every output written
-// once.  Memory bounds it, and the SwiGLU's arithmetic nearly as much (the vector units
-// were 90 % busy before places were worked out for a wave, and NaNs looked for beside the
-// clamps and maxima): T = 8192, I = 2048 SwiGLU (84 MB) 21.4 -> 19.2 us = 4.4 TB/s; T = 2047, K =
-// 4096 (25 MB) 6.6 -> 6.2 us = 4.1 TB/s.
+// once.  Memory bounds it: T = 8192, I = 2048 SwiGLU (84 MB) 17.3 us = 4.9 TB/s; T = 2047, K =
+// 4096 (25 MB) 6.2 us = 4.1 TB/s.  The SwiGLU's arithmetic is nearly as long: the vector
+// units were 97 % busy at 19.1 us, when the clamps had a branch and took the detour that
+// keeps a NaN; NaNs are now looked for beside them, into scalar masks.
 #include <hip/hip_runtime.h>
 
 #include "moe_wna16.h"
@@ -54,6 +54,14 @@ __device__ __forceinline__ float largest(float top, float a, float b)
 {
     float r;
     asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(r) : "v"(top), "v"(a), "v"(b));
+    return r;
+}
+
+// One instruction, where fminf takes a second for signalling NaNs.
+__device__ __forceinline__ float smaller(float a, float b)
+{
+    float r;
+    asm("v_min_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
 }
 
@@ -106,30 +114,26 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(QuantArgs a)
     const T *x = static_cast<const T *>(a.x) + at.x;
     float v[8];
     load8(x, left, v);
-    bool odd = false;                               // a NaN
+    uint64_t odd = 0;                               // lanes with a NaN
     if constexpr (SWIGLU) {
         float u[8];
         load8(x + a.n, left, u);
-        const bool clamped = a.clamp < INFINITY;
-        if (clamped) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {           // these drop a NaN
-                odd |= __builtin_isunordered(v[j], u[j]);
-                v[j] = __builtin_amdgcn_fmed3f(v[j], -INFINITY, a.clamp);
-                u[j] = __builtin_amdgcn_fmed3f(u[j], -a.clamp, a.clamp);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
+            odd |= __ballot(__builtin_isunordered(v[j], u[j]));
+            v[j] = smaller(v[j], a.clamp);          // these may drop a NaN
+            u[j] = __builtin_amdgcn_fmed3f(u[j], -a.clamp, a.clamp);
             v[j] = v[j] * sigmoid(a.alpha * v[j]) * (u[j] + a.beta);
+        }
     }
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-        odd |= __builtin_isunordered(v[j], v[j + 1]);
+        odd |= __ballot(__builtin_isunordered(v[j], v[j + 1]));
         most = largest(most, v[j], v[j + 1]);
     }
-    const uint32_t top = each_row_max(odd ? kInfBits : __float_as_uint(most));
+    const uint32_t top =
+        each_row_max(__builtin_amdgcn_inverse_ballot_w64(odd) ? kInfBits : __float_as_uint(most));
     const bool fine = top < kInfBits;
     const uint32_t e = scale_exponent(fine ? top : 0u);
     Codes8 q = to_e4m3(v, __uint_as_float((254u - e) << 23));
