@@ -357,34 +357,46 @@ struct TileF8 {
             return (unsigned)s < (unsigned)g.a_rows ? s : 0;
         };
         // Copy i of this wave brings rows [8 * (i * NW + wave), +8), of the tokens and
-        // then of the channels.  Rows past the end come as zeros (gathered ones as the last
-        // row); their results are dropped.
-        const int wlast = (g.N - n0 < BN ? g.N - n0 : BN) - 1;
-        const v4i abuf = GATHER ? buffer_of(g.a, (uint32_t)((long long)(g.a_rows - 1) * g.lda + g.K))
-                                : buffer_of(g.a + (long long)t0 * g.lda,
-                                            (uint32_t)((count - 1) * g.lda + g.K));
-        const v4i wbuf = buffer_of(w + (long long)n0 * g.ldw, (uint32_t)(wlast * g.ldw + g.K));
+        // then of the channels, each copy through a window of its own: rows past the end are
+        // outside it and not read.  (Gathered tokens: one window of all of a, and past the end
+        // the last row again.)  Their results are dropped.
+        const int wrows = g.N - n0 < BN ? g.N - n0 : BN;
         const int crow = lane >> 3;
         const int cplace = place(wave * 8 + crow, lane & 7) * 16;   // the same for every copy
+        v4i abuf[GATHER ? 1 : ACOPIES], wbuf[COPIES - ACOPIES];
         uint32_t aoff[GATHER ? ACOPIES : 1];
+        if constexpr (GATHER) {
+            abuf[0] = buffer_of(g.a, (uint32_t)((long long)(g.a_rows - 1) * g.lda + g.K));
 #pragma unroll
-        for (int i = 0; i < (GATHER ? ACOPIES : 1); ++i)
-            aoff[i] = (uint32_t)(GATHER ? a_row((i * NW + wave) * 8 + crow) : wave * 8 + crow) *
-                          (uint32_t)g.lda + (uint32_t)cplace;
-        const uint32_t woff = (uint32_t)(wave * 8 + crow) * (uint32_t)g.ldw + (uint32_t)cplace;
-        const uint32_t astep = GATHER ? 0u : NW * 8u * (uint32_t)g.lda, wstep = NW * 8u * (uint32_t)g.ldw;
-        // copy i of the chunk at byte k of the rows, to the stage at LDS address st
-        auto copy_one = [&](int i, uint32_t k, uint32_t st) {
+            for (int i = 0; i < ACOPIES; ++i)
+                aoff[i] = (uint32_t)a_row((i * NW + wave) * 8 + crow) * (uint32_t)g.lda + (uint32_t)cplace;
+        } else {
+            aoff[0] = (uint32_t)crow * (uint32_t)g.lda + (uint32_t)cplace;
+#pragma unroll
+            for (int i = 0; i < ACOPIES; ++i) {
+                const Window v = window_of((i * NW + wave) * 8, 8, count, (uint32_t)g.lda, (uint32_t)g.K);
+                abuf[i] = buffer_of(g.a + (long long)t0 * g.lda + v.start, v.bytes);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < COPIES - ACOPIES; ++i) {
+            const Window v = window_of((i * NW + wave) * 8, 8, wrows, (uint32_t)g.ldw, (uint32_t)g.K);
+            wbuf[i] = buffer_of(w + (long long)n0 * g.ldw + v.start, v.bytes);
+        }
+        const uint32_t woff = (uint32_t)crow * (uint32_t)g.ldw + (uint32_t)cplace;
+        // copy i of the rows' piece at byte k + back (back of the lane, k of the wave, which stays
+        // below K), to the stage at LDS address st
+        auto copy_one = [&](int i, uint32_t k, uint32_t st, uint32_t back = 0u) {
             if (i < ACOPIES)
-                copy16_to_lds(abuf, aoff[GATHER ? i : 0], i * astep + k, st + i * NW * 1024);
+                copy16_to_lds(abuf[GATHER ? 0 : i], aoff[GATHER ? i : 0] + back, k, st + i * NW * 1024);
             else
-                copy16_to_lds(wbuf, woff, (i - ACOPIES) * wstep + k, st + i * NW * 1024);
+                copy16_to_lds(wbuf[i - ACOPIES], woff + back, k, st + i * NW * 1024);
         };
         // Scale copy i of this wave: tokens [16 * (i * NW + wave), +16), four blocks
         // each; one more of wave 0, the weight's.  Blocks past the row's last one are
-        // somebody else's or zeros, and not used.
+        // somebody else's or outside the buffer, and not used.
         constexpr int SW = (SCOPIES + NW - 1) / NW;
-        const int kb = (g.K + KC - 1) / KC, wblocks = (n0 % 128 + wlast) / 128;
+        const int kb = (g.K + KC - 1) / KC, wblocks = (n0 % 128 + wrows - 1) / 128;
         const v4i asbuf = GATHER ? buffer_of(g.a_scale, (uint32_t)((g.a_rows - 1) * g.lda_s + kb) * 4u)
                                  : buffer_of(g.a_scale + (long long)t0 * g.lda_s,
                                              (uint32_t)((count - 1) * g.lda_s + kb) * 4u);
@@ -405,22 +417,19 @@ struct TileF8 {
 #pragma unroll
             for (int i = 0; i < SW; ++i)
                 if (i * NW + wave < SCOPIES)
-                    copy4_to_lds(asbuf, asoff[GATHER ? i : 0], i * asstep + (uint32_t)c * 4u,
+                    copy4_to_lds(asbuf, asoff[GATHER ? i : 0] + i * asstep + (uint32_t)c * 4u,
                                  buf + (uint32_t)((i * NW + wave) * 256));
             if (wave == 0 && lane < 4 * (SROWS - BM))
-                copy4_to_lds(wsbuf, wsoff, (uint32_t)c * 4u, buf + BM * 16);
+                copy4_to_lds(wsbuf, wsoff + (uint32_t)c * 4u, buf + BM * 16);
         };
         // The chunk that K (a multiple of 16) ends inside: past it the row's first piece
         // is read again, and the channel operand's registers are cleared below.
         auto copy_part = [&](int c) {
             const uint32_t st = lds0 + (c - c0) % ST * STAGE;
-            const uint32_t k = (uint32_t)(c * KC), back = c * KC + cplace < g.K ? k : 0u - cplace;
+            const uint32_t back = c * KC + cplace < g.K ? (uint32_t)(c * KC) : 0u - cplace;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i)
-                if (i < ACOPIES)
-                    copy16_to_lds(abuf, aoff[GATHER ? i : 0] + back, i * astep, st + i * NW * 1024);
-                else
-                    copy16_to_lds(wbuf, woff + back, (i - ACOPIES) * wstep, st + i * NW * 1024);
+                copy_one(i, 0u, st, back);
         };
         const int r = lane & 15, kq = lane >> 4;
         const int arow = wm * (MT * 16) + r, brow = BM + wn * (NT * 16) + r;

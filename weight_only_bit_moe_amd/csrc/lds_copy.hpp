@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "window.hpp"
+
 namespace wna16 {
 
 namespace {
@@ -36,8 +38,9 @@ __device__ __forceinline__ void copy16_to_lds(const void *base_in, uint32_t voff
                  : "memory", "m0");
 }
 
-// The same from a buffer: voff of the lane and soff of the wave are added, and
-// pieces past the buffer's end come as zeros.
+// The same from a buffer: voff of the lane and soff of the wave are added.  A piece at or
+// past the buffer's end by voff alone is not read; whether soff counts there too is not
+// relied on, so a piece inside by voff has to be inside with soff as well (window_of).
 __device__ __forceinline__ void copy16_to_lds(v4i buffer, uint32_t voff, uint32_t soff_in,
                                               uint32_t lds_in)
 {
@@ -47,14 +50,12 @@ __device__ __forceinline__ void copy16_to_lds(v4i buffer, uint32_t voff, uint32_
                  "s"(buffer), "s"(soff), "s"(lds)
                  : "memory", "m0");
 }
-// Each active lane l's 4 bytes land at lds + l * 4.
-__device__ __forceinline__ void copy4_to_lds(v4i buffer, uint32_t voff, uint32_t soff_in,
-                                             uint32_t lds_in)
+// Each active lane l's 4 bytes at voff land at lds + l * 4.
+__device__ __forceinline__ void copy4_to_lds(v4i buffer, uint32_t voff, uint32_t lds_in)
 {
     const uint32_t lds = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_in);
-    const uint32_t soff = (uint32_t)__builtin_amdgcn_readfirstlane((int)soff_in);
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff),
-                 "s"(buffer), "s"(soff), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff),
+                 "s"(buffer), "s"(lds)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
