@@ -87,6 +87,7 @@ struct Fp8Plan {
     size_t workspace;
 };
 Fp8Plan gemm_fp8_plan(int T, int N, int K);
+int gemm_fp8_grouped_tile(int experts, int R, int N, int K);
 hipError_t launch_gemm_fp8(const GemmFp8Args &a, const Fp8Plan &p, int out_dtype,
                            hipStream_t stream);
 hipError_t launch_gemm_fp8_grouped(const GemmFp8Args &a, int out_dtype, hipStream_t stream);

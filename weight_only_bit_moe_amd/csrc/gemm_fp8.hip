@@ -1071,8 +1071,6 @@ hipError_t launch_gemm_fp8(const GemmFp8Args &g, const Fp8Plan &p, int out_dtype
     return launch_stream<8, 4, 2>(g, out_dtype, stream);
 }
 
-namespace {
-
 // The tile of grouped products: rows are taken to be spread evenly, so that an
 // expert has half a row tile too much where it has several.  The weights are read
 // at 5.8 TB/s, again for each further row tile of an expert (at 12 TB/s, from the
@@ -1080,11 +1078,11 @@ namespace {
 // squares describes well: over 37 sizes (8 to 256 experts, 16 to 65536 rows) the
 // tiles that this picks take 0.1 % more than the best ones.  E = 256, N = K = 4096:
 // 64 x 128 and 128 x 256 with 16 rows an expert 727 and 776 us, with 64 960 and 825.
-int grouped_tile(const GemmFp8Args &g)
+int gemm_fp8_grouped_tile(int experts, int R, int N, int K)
 {
-    const float with_rows = (float)(g.experts < g.T ? g.experts : g.T);
-    const float rows = (float)g.T / with_rows;
-    const float weight = (float)g.N * (float)g.K;
+    const float with_rows = (float)(experts < R ? experts : R);
+    const float rows = (float)R / with_rows;
+    const float weight = (float)N * (float)K;
     int pick = 0;
     float best = INFINITY;
     for (int i = 0; i < kGroupedTiles; ++i) {
@@ -1092,7 +1090,7 @@ int grouped_tile(const GemmFp8Args &g)
         const float per = rows > 0.6f * c.bm ? fmaxf(1.f, rows / (float)c.bm + 0.5f) : 1.f;
         const float tiles = with_rows * per;
         const float compute = tile_cost(
-            c, (long long)tiles * ((g.N + c.bn - 1) / c.bn), (g.K + 127) / 128, 1);
+            c, (long long)tiles * ((N + c.bn - 1) / c.bn), (K + 127) / 128, 1);
         const float read = with_rows * weight / 5.8e6f + (tiles - with_rows) * weight / 12e6f;
         const float t = sqrtf(compute * compute + read * read);
         if (t < best) {
@@ -1103,11 +1101,9 @@ int grouped_tile(const GemmFp8Args &g)
     return pick;
 }
 
-}  // namespace
-
 hipError_t launch_gemm_fp8_grouped(const GemmFp8Args &g, int out_dtype, hipStream_t stream)
 {
-    return with_tile<kGroupedTiles>(grouped_tile(g), [&](auto tile) {
+    return with_tile<kGroupedTiles>(gemm_fp8_grouped_tile(g.experts, g.T, g.N, g.K), [&](auto tile) {
         return launch_grouped_tile<decltype(tile)>(g, out_dtype, stream);
     });
 }
