@@ -592,8 +592,8 @@ int moe_wna16_sort_tokens(const int32_t *ids, int T, int topk, int E, const void
  * dy [R, H] or NULL, dw [T, topk] float32 or NULL (then y may be NULL).  Rows of dy
  * that no slot names are not written, but with `used` (one int32 on the GPU,
  * sort_tokens' offsets + E) those from *used on are cleared.
- * 0 <= T <= 2^21 (0: no launch, for the gradient only without `used`), 0 <= R <= 2^24,
- * 1 <= topk <= 64, 1 <= H <= 2^20 (gradient: 32768).
+ * 0 <= T <= 2^21 (0: no launch; the gradient's only clears, where it has `used`),
+ * 0 <= R <= 2^24, 1 <= topk <= 64, 1 <= H <= 2^20 (gradient with T > 0: 32768).
  */
 int moe_wna16_combine_tokens(const void *y, const int32_t *slots, const float *weights,
                              const void *addend, int T, int topk, int H, int R, int64_t y_stride,

@@ -322,7 +322,7 @@ int moe_wna16_combine_tokens_grad(const void *dout, const void *y, const int32_t
     if (T < 0 || topk <= 0 || H <= 0 || R < 0 || !valid_dtype(dtype) || d_stride < H ||
         (dw && y_stride < H) || (dy && dy_stride < H) || (used && !dy && R > 0))
         return MOE_WNA16_EINVAL;
-    if (T > wna16::kMaxRows || topk > 64 || H > wna16::kMaxRow || R > kMaxPairs)
+    if (T > wna16::kMaxRows || topk > 64 || H > (T > 0 ? wna16::kMaxRow : kMaxColumns) || R > kMaxPairs)
         return MOE_WNA16_EUNSUPPORTED;
     if (T == 0 && (!used || R == 0))
         return MOE_WNA16_OK;

@@ -310,7 +310,9 @@ struct CombineNode : torch::autograd::Function<CombineNode> {
 
 // ---- sort and combine ------------------------------------------------------------
 
-// GRAPH: the result is part of x's graph.
+// GRAPH: the result is part of x's graph, and its rows behind the last sorted pair are
+// cleared: a function of all rows between sort and combine has gradients of its
+// parameters too, where their zeros meet those rows (0 * NaN is NaN).
 template <bool GRAPH>
 PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
 {
@@ -351,10 +353,15 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     if (lib.sort_tokens_workspace_size((int)T, (int)k, E, &bytes) == MOE_WNA16_OK && bytes)
         ws = empty({(int64_t)bytes}, at::kByte, dev);
     launch("moe_wna16_sort_tokens", dev, [&](hipStream_t s) {
-        return lib.sort_tokens((const int32_t *)ids.data_ptr(), (int)T, (int)k, E, xp, (int)H, xst,
-                               code, (int32_t *)tokens.data_ptr(), (int32_t *)slots.data_ptr(),
-                               (int32_t *)offsets.data_ptr(), xp ? xs.data_ptr() : nullptr, xsst,
-                               bytes ? ws.data_ptr() : nullptr, bytes, s);
+        const int st = lib.sort_tokens(
+            (const int32_t *)ids.data_ptr(), (int)T, (int)k, E, xp, (int)H, xst, code,
+            (int32_t *)tokens.data_ptr(), (int32_t *)slots.data_ptr(), (int32_t *)offsets.data_ptr(),
+            xp ? xs.data_ptr() : nullptr, xsst, bytes ? ws.data_ptr() : nullptr, bytes, s);
+        if (!GRAPH || st != MOE_WNA16_OK)
+            return st;
+        return lib.combine_tokens_grad(nullptr, nullptr, nullptr, nullptr,
+                                       (const int32_t *)offsets.data_ptr() + E, 0, (int)k, (int)H,
+                                       (int)P, H, H, xsst, code, xs.data_ptr(), nullptr, s);
     });
     if constexpr (GRAPH) {
         const variable_list v = SortNode::apply(tensor(p.v[2], "x"), (const Sorted *)&r);

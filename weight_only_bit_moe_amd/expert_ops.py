@@ -124,7 +124,8 @@ def sort_tokens(ids: torch.Tensor, experts: int, x: Optional[torch.Tensor] = Non
     "tokens" int32 [T * k], the token of each sorted pair, -1 behind the last; "slots" int32
     [T, k], the place of each pair, -1 for one left out; and, with x [T, H] (bf16, fp16 or fp32; rows
     may be strided), "x" [T * k, H], row tokens[i] of x at i.  Rows of "x" behind the last sorted
-    pair are not written.  out: memory for "x", not where x requires a gradient.
+    pair are not written; zeros where x requires a gradient.  out: memory for "x", not where x
+    requires a gradient.
 
     The gradient of x is the sum of its rows' (combine_tokens without weights)."""
     if _wants_grad(x):
