@@ -591,7 +591,8 @@ int moe_wna16_sort_tokens(const int32_t *ids, int T, int topk, int E, const void
  *   dw[t][j]        = <dout[t], y[slots[t][j]]> in FP32, 0 for a slot outside [0, R)
  * dy [R, H] or NULL, dw [T, topk] float32 or NULL (then y may be NULL).  Rows of dy
  * that no slot names are not written, but with `used` (one int32 on the GPU,
- * sort_tokens' offsets + E) those from *used on are cleared.
+ * sort_tokens' offsets + E) those from *used on are cleared, also where a slot
+ * names one.
  * 0 <= T <= 2^21 (0: no launch; the gradient's only clears, where it has `used`),
  * 0 <= R <= 2^24, 1 <= topk <= 64, 1 <= H <= 2^20 (gradient with T > 0: 32768).
  */

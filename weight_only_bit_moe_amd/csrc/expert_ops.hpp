@@ -57,7 +57,7 @@ struct CombineGradArgs {
     const void *dout, *y;                       // [T], [R] rows of H; y null: no dw
     const int32_t *slots;
     const float *weights;                       // or null: ones
-    const int32_t *used;                        // device: rows from *used on get zeros; or null
+    const int32_t *used;                        // device: dy's rows from *used on get zeros; or null
     long long d_stride, y_stride, dy_stride;
     int T, topk, H, R;
     int threads;

@@ -462,10 +462,11 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
 {
     __shared__ float part[64][16];
     const int threads = a.threads;
+    // rows of dy from here on are cleared, and only that: a slot there gets nothing
+    const int used = !a.used ? a.R : *a.used < 0 ? 0 : *a.used < a.R ? *a.used : a.R;
     if ((int)blockIdx.x >= a.T) {
-        const int used = *a.used;
         const float zero[8] = {};
-        for (int s = (used < 0 ? 0 : used) + (int)blockIdx.x - a.T; s < a.R; s += kClearGroups) {
+        for (int s = used + (int)blockIdx.x - a.T; s < a.R; s += kClearGroups) {
             T *o = static_cast<T *>(a.dy) + s * a.dy_stride;
             for (int c = (int)threadIdx.x * 8; c < a.H; c += threads * 8)
                 store8(o + c, a.H - c, zero);
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a)
             for (int i = 0; i < R; ++i)
                 v[i] = next[i];
         }
-        if (a.dy && s >= 0) {
+        if (a.dy && s >= 0 && s < used) {
             const float w =
                 __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weights_at), j));
             T *o = static_cast<T *>(a.dy) + s * a.dy_stride;

@@ -148,8 +148,10 @@ def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch
     of y and the addend may be strided.  out may be the addend; not where a gradient is required.
 
     Gradients of y, weights and the addend; for those no two slots may name the same row of y.
-    offsets: sort_tokens', with which only y's rows behind the last sorted one are cleared in its
-    gradient; without, all of it is first."""
+    Rows of y that no slot names have a gradient of zero.  offsets: sort_tokens', where its slots are
+    used as they are: then only the gradient's rows behind the last sorted one are cleared, and each
+    before it has to be named by a slot.  Where pairs have been left out since (slots set to -1),
+    give none: all of the gradient is cleared first."""
     if _wants_grad(y, weights, addend):
         if out is not None:
             raise ValueError("out is given, and a gradient is required")
