@@ -262,20 +262,27 @@ struct Combined {
 struct CombineNode : torch::autograd::Function<CombineNode> {
     static variable_list forward(AutogradContext *ctx, const at::Tensor &y,
                                  const std::optional<at::Tensor> &weights,
-                                 const std::optional<at::Tensor> &, const Combined *c)
+                                 const std::optional<at::Tensor> &addend, const Combined *c)
     {
         ctx->set_materialize_grads(false);
         ctx->save_for_backward({c->weights ? y : at::Tensor(), c->slots,
                                 weights ? *weights : at::Tensor(), c->offsets});
         ctx->saved_data["rows"] = y.size(0);
         ctx->saved_data["wanted"] = (int64_t)(c->y + 2 * c->weights + 4 * c->addend);
+        ctx->saved_data["given"] = (int64_t)(1 + 2 * weights.has_value() + 4 * addend.has_value());
         return {c->out};
     }
     static variable_list backward(AutogradContext *ctx, variable_list grads)
     {
         if (!grads[0].defined())
             return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
-        const int64_t wanted = ctx->saved_data["wanted"].toInt(), R = ctx->saved_data["rows"].toInt();
+        // which require a gradient, and of these (in order) which this call is asked for
+        int64_t wanted = ctx->saved_data["wanted"].toInt();
+        const int64_t R = ctx->saved_data["rows"].toInt();
+        const int64_t given = ctx->saved_data["given"].toInt();
+        for (int i = 0, edge = 0; i < 3; ++i)
+            if (given >> i & 1 && !ctx->needs_input_grad(edge++))
+                wanted &= ~(1ll << i);
         const variable_list saved = ctx->get_saved_variables();
         const at::Tensor &y = saved[0], &slots = saved[1], &weights = saved[2], &offsets = saved[3];
         at::Tensor dy, dw;
