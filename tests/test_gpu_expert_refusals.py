@@ -1,0 +1,28 @@
+"""Calls of the operators for experts in 8-bit floating point that are refused before anything runs."""
+import pytest
+import torch
+
+import weight_only_bit_moe_amd as M
+from tests.test_gpu_expert_grads import case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    return torch.device("cuda:0")
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_offsets_are_checked_with_and_without_a_gradient(dev, grad):
+    ids, x, w, E = case(dev)
+    s = M.sort_tokens(ids, E, x.detach())
+    y, off = s["x"].requires_grad_(grad), s["offsets"]
+    for bad, kind in ((off.long(), TypeError), (off.cpu(), ValueError), (off[:0], ValueError), (off[::2], ValueError),
+                      ([0, 1], TypeError)):
+        out = torch.full_like(x.detach(), 7.0)
+        with pytest.raises(kind):
+            M.combine_tokens(y, s["slots"], offsets=bad, **({} if grad else dict(out=out)))
+        assert bool((out == 7).all())
+    assert M.combine_tokens(y, s["slots"], offsets=off).requires_grad == grad

@@ -406,6 +406,12 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     check(slots, "slots", {T, k}, at::kInt, dev);
     const int64_t ys = rows(y, "y", {R, H}, dt, dev);
     const void *wp = optional_flat(p.v[2], "weights", {T, k}, at::kFloat, dev);
+    if (p.v[5]) {
+        const at::Tensor &offsets = tensor(p.v[5], "offsets");
+        flat(offsets, "offsets", {offsets.numel()}, at::kInt, dev);
+        if (offsets.numel() < 1)
+            fail(PyExc_ValueError, "offsets is empty");
+    }
     const void *ap = nullptr;
     int64_t as = H;
     if (p.v[3]) {
@@ -428,12 +434,8 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
         const std::optional<at::Tensor> w = given(2), add = given(3);
         Combined c{slots, {}, out, y.requires_grad(), w && w->requires_grad(),
                    add && add->requires_grad()};
-        if (p.v[5]) {
+        if (p.v[5])
             c.offsets = tensor(p.v[5], "offsets");
-            flat(c.offsets, "offsets", {c.offsets.numel()}, at::kInt, dev);
-            if (c.offsets.numel() < 1)
-                fail(PyExc_ValueError, "offsets is empty");
-        }
         out = CombineNode::apply(y, w, add, (const Combined *)&c)[0];
     }
     return THPVariable_Wrap(out);

@@ -156,7 +156,7 @@ def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch
         if out is not None:
             raise ValueError("out is given, and a gradient is required")
         return _block_ops.combine_tokens_graph(y, slots, weights, addend=addend, offsets=offsets)
-    return _block_ops.combine_tokens(y, slots, weights, addend=addend, out=out)
+    return _block_ops.combine_tokens(y, slots, weights, addend=addend, out=out, offsets=offsets)
 
 
 def forward_fp8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
