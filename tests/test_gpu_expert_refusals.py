@@ -26,3 +26,20 @@ def test_offsets_are_checked_with_and_without_a_gradient(dev, grad):
             M.combine_tokens(y, s["slots"], offsets=bad, **({} if grad else dict(out=out)))
         assert bool((out == 7).all())
     assert M.combine_tokens(y, s["slots"], offsets=off).requires_grad == grad
+
+
+def test_rows_too_long_for_a_gradient_are_refused_at_the_call(dev):
+    H = 32769
+    y, w, add = torch.randn(4, H, device=dev), torch.ones(2, 2, device=dev), torch.randn(2, H, device=dev)
+    slots = torch.arange(4, dtype=torch.int32, device=dev).view(2, 2)
+    for a, b in ((y.clone().requires_grad_(), w), (y, w.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="up to 32768"):
+            M.combine_tokens(a, slots, b)
+        with torch.no_grad():
+            assert M.combine_tokens(a, slots, b).shape == (2, H)
+    added = add.clone().requires_grad_()                # its gradient is the output's, of any length
+    M.combine_tokens(y, slots, w, addend=added).sum().backward()
+    assert torch.equal(added.grad, torch.ones_like(add))
+    a = y[:, 1:].clone().requires_grad_()
+    M.combine_tokens(a, slots, w).sum().backward()
+    assert torch.equal(a.grad, torch.ones_like(a))

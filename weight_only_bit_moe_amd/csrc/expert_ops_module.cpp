@@ -19,6 +19,8 @@ PyObject *n_x, *n_q, *n_scale, *n_gu, *n_alpha, *n_beta, *n_clamp, *n_a, *n_a_sc
     *n_w_scale, *n_addend, *n_out_dtype, *n_out, *n_workspace, *n_offsets, *n_rows, *n_ids,
     *n_experts, *n_tokens, *n_slots, *n_y, *n_weights;
 
+constexpr int64_t kMaxGradientRow = 32768;          // moe_wna16_combine_tokens_grad's
+
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
 at::ScalarType out_type(PyObject *o)
@@ -419,6 +421,11 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
         as = rows(add, "addend", {T, H}, dt, dev);
         ap = add.data_ptr();
     }
+    if constexpr (GRAPH)            // here, not in the gradient
+        if (H > kMaxGradientRow &&
+            (y.requires_grad() || (p.v[2] && tensor(p.v[2], "weights").requires_grad())))
+            fail(PyExc_ValueError, "y has rows of %lld elements, gradients are for up to %lld",
+                 (long long)H, (long long)kMaxGradientRow);
     ensure_library();
     at::Tensor out = given_or_empty(p.v[4], "out", {T, H}, dt, dev);
     const int64_t os = rows(out, "out", {T, H}, dt, dev);

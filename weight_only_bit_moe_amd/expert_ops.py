@@ -146,6 +146,7 @@ def combine_tokens(y: torch.Tensor, slots: torch.Tensor, weights: Optional[torch
     y [R, H] (bf16, fp16 or fp32), slots int32 [T, k] as sort_tokens returns them (those outside
     [0, R) are left out), weights float32 [T, k] (ones without), addend [T, H] of y's type; rows
     of y and the addend may be strided.  out may be the addend; not where a gradient is required.
+    H up to 2^20, with a gradient of y or the weights 32768.
 
     Gradients of y, weights and the addend; for those no two slots may name the same row of y.
     Rows of y that no slot names have a gradient of zero.  offsets: sort_tokens', where its slots are
