@@ -43,3 +43,23 @@ def test_rows_too_long_for_a_gradient_are_refused_at_the_call(dev):
     a = y[:, 1:].clone().requires_grad_()
     M.combine_tokens(a, slots, w).sum().backward()
     assert torch.equal(a.grad, torch.ones_like(a))
+
+
+def test_forward_mode_is_refused(dev):
+    import torch.autograd.forward_ad as forward
+    ids, x, w, E = case(dev)
+    x, w = x.detach(), w.detach()
+    s = M.sort_tokens(ids, E, x)
+    y, slots = s["x"], s["slots"]
+    with forward.dual_level():
+        for asked in (False, True):
+            def dual(t):
+                return forward.make_dual(t.clone().requires_grad_(asked), torch.ones_like(t))
+            for call in (lambda: M.sort_tokens(ids, E, dual(x)), lambda: M.combine_tokens(dual(y), slots, w),
+                         lambda: M.combine_tokens(y, slots, dual(w)), lambda: M.combine_tokens(y, slots, w, addend=dual(x))):
+                with pytest.raises(NotImplementedError, match="tangent"):
+                    call()
+                with torch.no_grad(), pytest.raises(NotImplementedError, match="tangent"):
+                    call()
+        assert torch.equal(M.sort_tokens(ids, E, x)["x"], y)        # without one, inside a level
+    assert torch.equal(M.sort_tokens(ids, E, x)["x"], y)

@@ -319,6 +319,14 @@ struct CombineNode : torch::autograd::Function<CombineNode> {
 
 // ---- sort and combine ------------------------------------------------------------
 
+// They have reverse-mode gradients only: a tangent would be dropped without a word.
+void no_tangent(const at::Tensor &t, const char *fn, const char *name)
+{
+    if (t._fw_grad(0).defined())
+        fail(PyExc_NotImplementedError, "%s() has no forward-mode derivative, and %s has a tangent", fn,
+             name);
+}
+
 // GRAPH: the result is part of x's graph, and its rows behind the last sorted pair are
 // cleared: a function of all rows between sort and combine has gradients of its
 // parameters too, where their zeros meet those rows (0 * NaN is NaN).
@@ -343,6 +351,7 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     int code = MOE_WNA16_BF16;
     if (p.v[2]) {
         const at::Tensor &x = matrix(p.v[2], "x");
+        no_tangent(x, "sort_tokens", "x");
         H = x.size(1);
         code = dtype_code(x.scalar_type(), "x");
         xst = rows(x, "x", {T, H}, x.scalar_type(), dev);
@@ -406,8 +415,11 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     if (H < 1 || k < 1)
         fail(PyExc_ValueError, "y has no columns, or slots names no rows");
     check(slots, "slots", {T, k}, at::kInt, dev);
+    no_tangent(y, "combine_tokens", "y");
     const int64_t ys = rows(y, "y", {R, H}, dt, dev);
     const void *wp = optional_flat(p.v[2], "weights", {T, k}, at::kFloat, dev);
+    if (p.v[2])
+        no_tangent(tensor(p.v[2], "weights"), "combine_tokens", "weights");
     if (p.v[5]) {
         const at::Tensor &offsets = tensor(p.v[5], "offsets");
         flat(offsets, "offsets", {offsets.numel()}, at::kInt, dev);
@@ -418,6 +430,7 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
     int64_t as = H;
     if (p.v[3]) {
         const at::Tensor &add = tensor(p.v[3], "addend");
+        no_tangent(add, "combine_tokens", "addend");
         as = rows(add, "addend", {T, H}, dt, dev);
         ap = add.data_ptr();
     }

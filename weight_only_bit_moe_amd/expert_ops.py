@@ -13,9 +13,10 @@ allocation and the library call are in the compiled module _block_ops, as for th
 operators around the layer.  The raw entry points take integer device addresses.
 
 sort_tokens and combine_tokens give gradients to x, y, the weights and the addend where they
-require one (a gradient's own graph is refused); the others take tensors as values.  A step captured
-into a graph has its forward and its backward in the one capture, and no eager graph of the same
-leaves may be alive then: torch ends the process over the stream it was made on.
+require one (a gradient's own graph is refused, and so is a forward-mode tangent of theirs); the
+others take tensors as values.  A step captured into a graph has its forward and its backward in the
+one capture, and no eager graph of the same leaves may be alive then: torch ends the process over the
+stream it was made on.
 """
 from __future__ import annotations
 
