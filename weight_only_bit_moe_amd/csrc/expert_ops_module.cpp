@@ -327,6 +327,13 @@ void no_tangent(const at::Tensor &t, const char *fn, const char *name)
              name);
 }
 
+// Values written into a tensor with a graph would leave it the gradient of the old ones.
+void not_in_a_graph(PyObject *out)
+{
+    if (out && at::GradMode::is_enabled() && tensor(out, "out").requires_grad())
+        fail(PyExc_ValueError, "out requires a gradient");
+}
+
 // GRAPH: the result is part of x's graph, and its rows behind the last sorted pair are
 // cleared: a function of all rows between sort and combine has gradients of its
 // parameters too, where their zeros meet those rows (0 * NaN is NaN).
@@ -358,6 +365,7 @@ PyObject *sort_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
         xp = x.data_ptr();
         if (H < 1)
             fail(PyExc_ValueError, "x has no columns");
+        not_in_a_graph(p.v[3]);
         xs = given_or_empty(p.v[3], "out", {P, H}, x.scalar_type(), dev);
         xsst = rows(xs, "out", {P, H}, x.scalar_type(), dev);
     } else if (p.v[3]) {
@@ -439,6 +447,7 @@ PyObject *combine_tokens(PyObject *const *args, Py_ssize_t nargs, PyObject *kw)
             (y.requires_grad() || (p.v[2] && tensor(p.v[2], "weights").requires_grad())))
             fail(PyExc_ValueError, "y has rows of %lld elements, gradients are for up to %lld",
                  (long long)H, (long long)kMaxGradientRow);
+    not_in_a_graph(p.v[4]);
     ensure_library();
     at::Tensor out = given_or_empty(p.v[4], "out", {T, H}, dt, dev);
     const int64_t os = rows(out, "out", {T, H}, dt, dev);

@@ -178,11 +178,17 @@ inline at::Tensor fresh_workspace(int64_t bytes, c10::Device dev)
     return t;
 }
 
-// The caller's tensor, or a new one.
+// The caller's tensor, or a new one.  The caller's counts as changed: a graph that
+// has kept it for its gradient says so instead of using the new values.
 inline at::Tensor given_or_empty(PyObject *o, const char *name, c10::IntArrayRef shape,
                           at::ScalarType dtype, c10::Device dev)
 {
-    return o ? tensor(o, name) : empty(shape, dtype, dev);
+    if (!o)
+        return empty(shape, dtype, dev);
+    const at::Tensor &t = tensor(o, name);
+    if (t.defined() && !t.is_inference())
+        t.unsafeGetTensorImpl()->bump_version();
+    return t;
 }
 
 inline double number(PyObject *o, double otherwise)
