@@ -63,3 +63,24 @@ def test_forward_mode_is_refused(dev):
                     call()
         assert torch.equal(M.sort_tokens(ids, E, x)["x"], y)        # without one, inside a level
     assert torch.equal(M.sort_tokens(ids, E, x)["x"], y)
+
+
+def test_the_layer_checks_its_arguments_against_each_other(dev):
+    from tests.test_gpu_expert_layer import experts
+    (w13, s13, w2, s2), g = experts("sizes", 4, 64, 32, dev)
+    x = torch.randn(5, 64, generator=g).bfloat16().to(dev)
+    ids, w = torch.zeros(5, 2, dtype=torch.int32, device=dev), torch.ones(5, 2, device=dev)
+    full = M.forward_fp8(x, ids, w, w13, s13, w2, s2)
+    assert torch.equal(M.forward_fp8(x, ids, w, w13, s13, w2, s2, codes=M.quant_fp8(x)), full)
+    more = lambda t: torch.cat([t, t[:2]])  # noqa: E731
+    for call in (lambda: M.forward_fp8(x, ids[:3], w[:3], w13, s13, w2, s2), lambda: M.forward_fp8(x, more(ids), more(w), w13, s13, w2, s2),
+                 lambda: M.forward_fp8(x, ids, w, w13, s13, w2, s2, codes=M.quant_fp8(more(x))),
+                 lambda: M.forward_fp8(x, ids, w, w13, s13, w2, s2, codes=M.quant_fp8(x[:4])),
+                 lambda: M.forward_fp8(x, ids, w, w13, s13, w2[:, :48], s2), lambda: M.forward_fp8(x, ids, w, w13, s13, w2[:3], s2[:3]),
+                 lambda: M.forward_fp8(x, ids, w, w13, s13, w2[..., :16], s2), lambda: M.forward_fp8(x, ids, w, w13[0], s13, w2, s2),
+                 lambda: M.forward_fp8(x, ids, w[:, :1], w13, s13, w2, s2), lambda: M.forward_fp8(x, ids, w, w13, s13, w2, s2, addend=x[:4]),
+                 lambda: M.forward_fp8(x, ids, w, w13, s13, w2, s2, out=more(x))):
+        with pytest.raises(ValueError):
+            call()
+    # codes of a view with its tokens' own rows
+    assert torch.equal(M.forward_fp8(x[1:4], ids[1:4], w[1:4], w13, s13, w2, s2), full[1:4])

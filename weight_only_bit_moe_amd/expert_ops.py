@@ -180,6 +180,14 @@ def forward_fp8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w
     T * k up to 2^21, T * H below 2^32."""
     q, scale = quant_fp8(x) if codes is None else codes
     s = _block_ops.sort_tokens(topk_ids, w13.shape[0])
+    # what no single operator sees: rows of other tokens would be read, or left out
+    T, H = x.shape
+    if topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids has {topk_ids.shape[0]} rows, x {T}")
+    if q.shape != x.shape:
+        raise ValueError("codes are of another shape than x")
+    if w13.dim() != 3 or w2.shape != (w13.shape[0], H, w13.shape[1] // 2):
+        raise ValueError("w2 must be [E, H, I] where w13 is [E, 2I, H]")
     gu = gemm_fp8_grouped(q, scale, w13, w13_scale, s["offsets"], rows=s["tokens"], out_dtype=x.dtype)
     q, scale = swiglu_quant_fp8(gu, alpha=alpha, beta=beta, clamp=clamp)
     y = gemm_fp8_grouped(q, scale, w2, w2_scale, s["offsets"], out_dtype=x.dtype)
