@@ -512,8 +512,9 @@ int moe_wna16_swiglu_quant_fp8(const void *gu, int T, int I, int64_t gu_stride, 
  * Product of such rows with such a weight:
  *   out[t][n] = sum_b a_scale[t][b] w_scale[n / 128][b] sum_{k in b} a[t][k] w[n][k]
  *               + addend[t][n]
- * FP32 sums, rounded once to out_dtype.  The same call gives the same bits.  The
- * matrix instruction lines the products of eight consecutive k (from a multiple of
+ * FP32 sums, rounded once to out_dtype.  The two scales are multiplied first, in FP32:
+ * their product has to be finite, and counts in full from 2^-126 on.  The same call
+ * gives the same bits.  The matrix instruction lines the products of eight consecutive k (from a multiple of
  * eight) up to the largest sum E of two codes' exponents (at least -6 each) among
  * them and drops what lies below 2^(E - 13): less than 7 * 2^-13 * 2^E of eight
  * products, about 1.5e-5 of a result of ordinary data, which only out_dtype float32

@@ -13,14 +13,17 @@
 // takes no scales: there is no more exact one in 8 bits.  About 1.5e-5 of a result with
 // ordinary data, 1/250 of a bf16 step.
 //
-// Bounds: up to 32 tokens the bytes of the weight (T = 4, N = K = 4096 4.6 us = 3.7 TB/s,
-// where launch and the first bytes' latency are half); past some hundred tokens the LDS
-// and the matrix cores alike (T = 8192, N = K = 4096 117 us = 2.3 PFLOP/s; 65536 rows of 32
-// experts 2.2 PFLOP/s); grouped, the weights of the experts that have rows (T = 4, 24 of
-// them 74 us = 5.4 TB/s; T = 64, 200 of 2048 x 4096 231 us), or with some 256 rows an expert
-// both at once (4.3 GB and 2.2 TFLOP 1500 us; 1290 where every expert has 256 rows).
+// Bounds (a pass among others; alone in a kernel trace the medians are up to 9 % longer):
+// up to 32 tokens the bytes of the weight (T = 4, N = K = 4096 4.6 us = 3.7 TB/s, where
+// launch and the first bytes' latency are half); past some hundred tokens the LDS and the
+// matrix cores alike (2048 cycles a block each with tiles of 256 x 256), and with all CUs at
+// work something that they share, the clock under load or the fabric (T = 8192, N = K = 4096
+// 119-126 us = 2.2-2.3 PFLOP/s; 65536 rows of 32 experts 2.2 PFLOP/s); grouped, the weights of the
+// experts that have rows (T = 4, 24 of them 71-74 us = 5.4 TB/s; T = 64, 200 of 2048 x 4096
+// 227-237 us), or with some 256 rows an expert both at once (4.3 GB and 2.2 TFLOP 1540 us; 1320
+// where every expert has 256 rows: a quarter of the products are past the experts' ends).
 // Rows that begin inside a cache line of 128 bytes cost twice its reads: T = 2047, N = 2057,
-// K = 4096 27.5 us, K = 4048 34.
+// K = 4096 26.9 us, K = 4048 30.2.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -948,10 +951,11 @@ hipError_t launch_grouped_tile(const GemmFp8Args &g, int out_dtype, hipStream_t 
 // 512 to 4096, K 1024 to 4096; most within 4 %); over them the tiles that it picks
 // take 0.5 % more than the best ones.
 //
-// LDS bounds the loop: a wave reads its tile's rows and channels for every block,
+// LDS bounds the loop of one CU: a wave reads its tile's rows and channels for every block,
 // and the copies write each once, at 128 bytes a cycle.  128 x 64 a wave (256 x
-// 256) makes that as long as the MFMAs (2048 cycles a block; about 2700 measured),
-// 64 x 64 (128 x 256) longer, 64 x 32 twice as long.  The small tiles are for few
+// 256) makes that as long as the MFMAs (2048 cycles a block; with few CUs about 2700
+// measured, with all of them 1.7 times that long), 64 x 64 (128 x 256) longer, 64 x 32
+// twice as long.  The small tiles are for few
 // rows: they cover them with more CUs.  A wave whose rows or channels are all past the
 // end only copies, so that a part of a tile costs less (E = 256, 65536 rows, N = K =
 // 4096: 1588 -> 1498 us).  Two workgroups of 128 x 128 with four waves a

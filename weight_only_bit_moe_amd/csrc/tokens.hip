@@ -11,7 +11,7 @@
 //
 // The rows are the bulk: each token's row is read once, into registers, and
 // written to its topk places, so memory's write rate bounds it.  T = 4096, k = 8, H =
-// 4096 (302 MB) 64 us = 4.7 TB/s, of which the slots take 9 on their own; T = 65536, k =
+// 4096 (302 MB) 68 us = 4.4 TB/s, of which the slots take 9 on their own; T = 65536, k =
 // 8, H = 1024 (1.2 GB) 237 us = 5.1 TB/s; T = 64, k = 6, H = 4096 4 us, most of it the launch
 // and one trip to memory for the ids and one for the rows.
 #include <hip/hip_runtime.h>
@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(1024) combine_kernel(CombineArgs a)
 // The gradients:  dy[slot[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[slot[t][j]]>.
 // A workgroup owns a token and holds its row of dout; each row of y is read and
 // each row of dy written once.  Workgroups behind the tokens clear the rows of dy
-// that no token has.  Bytes bound it: T = 4096, k = 8, H = 4096 (570 MB) 99 us = 5.7 TB/s;
-// combine_kernel there (302 MB) 56 us = 5.4 TB/s.  The dot products are FP32: eight elements
+// that no token has.  Bytes bound it: T = 4096, k = 8, H = 4096 (570 MB) 100 us = 5.7 TB/s;
+// combine_kernel there (302 MB) 58 us = 5.2 TB/s.  The dot products are FP32: eight elements
 // in order, then the rows' pieces, lanes and waves in a fixed order.
 constexpr int kClearGroups = 256;
 
