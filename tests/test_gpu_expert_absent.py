@@ -87,3 +87,41 @@ def test_captured(dev):
         want = M.sort_tokens(data[i % 4], E, x)
         n = int(want["offsets"][-1])
         assert torch.equal(s["x"][:n], want["x"][:n]) and not s["x"][n:].any()
+
+
+@pytest.mark.parametrize("T,k,E", [(40, 4, 8), (3000, 4, 64)])
+def test_captured_training_step(dev, T, k, E):
+    """Sort, a function of all rows with parameters, combine and their gradients in one graph, with other
+    pairs left out in each replay, against the eager step."""
+    H = 96
+    g = gen("absent step", T)
+    # a parameter for each row, so that no sum of torch's is in the graph
+    d, scale = torch.randn(T, H, generator=g).to(dev), torch.randn(T * k, H, generator=g).to(dev)
+
+    def step(ids, x, w, p):
+        s = M.sort_tokens(ids, E, x)
+        out = M.combine_tokens(torch.tanh(s["x"] * p), s["slots"], w, offsets=s["offsets"])
+        return (out, *torch.autograd.grad(out, (x, w, p), d))
+
+    data = [(some_ids((i, "step"), T, k, E).to(dev), torch.randn(T, H, generator=g).to(dev),
+             torch.rand(T, k, generator=g).to(dev), scale * (i + 1)) for i in range(3)]
+    leaves = lambda c: (c[0].clone(), *(t.clone().requires_grad_() for t in c[1:]))  # noqa: E731
+    want = [step(*leaves(c)) for c in data]
+    held = leaves(data[0])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(*held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(*held)
+    for i in range(7):
+        with torch.no_grad():
+            for a, b in zip(held, data[i % 3]):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step(*leaves(data[(i + 1) % 3]))
+        torch.cuda.synchronize()
+        for a, b in zip((*outs, *eager), (*want[i % 3], *want[(i + 1) % 3])):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
